@@ -151,6 +151,17 @@ gdn::VerifyArgs make_args(const gdn_dims &d, int n_tok, int n_batch)
 
 namespace gdn {
 int abi_check_dims(const gdn_dims *d) { return check_dims(d); }
+
+int abi_fetch_i32(const int32_t *dev, size_t n, hipStream_t st, int32_t *out)
+{
+    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(st, &cs) != hipSuccess || cs != hipStreamCaptureStatusNone)
+        return fail(GDN_ERR_ARG, "GDN_F_CHECK_INDICES copies indices to the host, which a capturing stream cannot do");
+    hipError_t e = hipMemcpyAsync(out, dev, n * sizeof(int32_t), hipMemcpyDeviceToHost, st);
+    if (e == hipSuccess) e = hipStreamSynchronize(st);
+    if (e != hipSuccess) return hip_fail(e, "index check copy");
+    return GDN_OK;
+}
 }  // namespace gdn
 
 namespace {

@@ -6,6 +6,10 @@
 #include <stdint.h>
 
 struct gdn_dims;  // include/gdn.h
+struct gdn_kv;
+struct gdn_kv_batch;
+struct gdn_rope_table;
+struct gdn_rows;
 
 namespace gdn {
 
@@ -114,6 +118,77 @@ struct LinearArgs {
     LinearSeg seg[kMaxLinearSegs];
 };
 hipError_t launch_linear(const LinearArgs &a, hipStream_t stream);
+
+// ---- full-attention layers: rotary positions, paged KV cache, attention ----
+
+// gdn_rope_table as the kernels take it (by value).
+constexpr int kMaxRopePairs = 128;
+struct RopeTab {
+    int32_t rot, pairs, interleaved, n_axes;
+    int32_t axis_end[4];
+    float mscale;
+    double turns[kMaxRopePairs];
+};
+struct RowsView {
+    void *p;
+    int64_t ld, hd;
+    int32_t bf16;
+};
+constexpr int kMaxRopeSegs = 4;
+struct RopeSeg {
+    RowsView x, out;
+    int32_t n_heads, in_place;
+};
+struct RopeArgs {
+    RopeTab tab;
+    RopeSeg seg[kMaxRopeSegs];
+    int32_t n_segs, d, heads, inverse;  // heads: of all segments together
+    int32_t n_tok, t0, nt;              // tokens of the call (the positions' axis stride) and of one launch
+    const int32_t *positions;
+};
+hipError_t launch_rope(const RopeArgs &a, hipStream_t stream);
+
+enum { kKvBf16 = 0, kKvE4m3 = 1, kKvI8 = 2 };  // gdn_kv_format
+struct KvView {
+    unsigned char *k, *v;
+    float *ks, *vs;
+    int32_t n_kv, d, shift, n_pages, format;  // page_size = 1 << shift
+};
+struct KvBatchView {
+    const int32_t *table, *start, *n_new;
+    int32_t max_pages, n_batch, n_tok;
+};
+struct KvRowsArgs {
+    KvView kv;
+    KvBatchView b;
+    RowsView k, v;
+    const int32_t *positions;  // [n_axes][n_batch * n_tok]; used when rope is set
+    int32_t rope;
+    RopeTab tab;
+};
+hipError_t launch_kv_write(const KvRowsArgs &a, hipStream_t stream);
+hipError_t launch_kv_read(const KvRowsArgs &a, hipStream_t stream);
+struct KvCommitArgs {
+    KvView kv;
+    KvBatchView b;
+    const int32_t *path, *n_path;
+    int32_t max_path;
+};
+hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t stream);
+// Checks shared by the cache's entry points (gdn_kv_abi.cpp); each sets the last error.
+int abi_check_kv(const char *fn, const gdn_kv *kv, bool pointers);
+int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_heads);  // aligned rows
+int abi_check_batch(const char *fn, const gdn_kv_batch *b);
+// Under GDN_F_CHECK_INDICES: the batch's arrays, copied to the host, name places that exist, for
+// positions [0, start + n) (from_zero) or [start, start + n).
+int abi_check_places(const char *fn, const gdn_kv *kv, const gdn_kv_batch *b, bool from_zero, hipStream_t st);
+KvView kv_view(const gdn_kv &kv);
+KvBatchView kv_batch_view(const gdn_kv_batch &b);
+RowsView rows_view(const gdn_rows &r);
+
+// Host copy of n device int32 for GDN_F_CHECK_INDICES (synchronises with st; a capturing stream is
+// refused untouched).  Sets the last error; GDN_OK if the copy was made.
+int abi_fetch_i32(const int32_t *dev, size_t n, hipStream_t st, int32_t *out);
 
 // The C ABI's thread-local last error (gdn_last_error): set it and return code, or clear it and
 // return GDN_OK.

@@ -20,11 +20,15 @@ GDN_CHAIN, GDN_TREE = 0, 1
 GDN_F_QK_NORM_SILU = 0x1
 GDN_F_CHECK_INDICES = 0x2
 GDN_F_DEFER_COMMIT = 0x4
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_YARN = range(4)
+GDN_KV_BF16, GDN_KV_E4M3, GDN_KV_I8 = range(3)
 
 EXPORTS = ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_batch", "gdn_rollback_trim",
            "gdn_prefill", "gdn_prefill_noalloc", "gdn_prefill_workspace_bytes", "gdn_capture_bytes", "gdn_reset",
            "gdn_snapshot", "gdn_restore", "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch",
-           "gdn_graph_destroy", "gdn_linear", "gdn_last_error", "gdn_version")
+           "gdn_graph_destroy", "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_bytes", "gdn_kv_write",
+           "gdn_kv_read", "gdn_kv_commit", "gdn_last_error", "gdn_version")
 
 
 class GdnError(RuntimeError):
@@ -54,6 +58,35 @@ class gdn_layer(ctypes.Structure):
 class gdn_out_seg(ctypes.Structure):
     _fields_ = [("n0", ctypes.c_int32), ("n1", ctypes.c_int32), ("ld", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("ptr", ctypes.c_void_p)]
+
+
+class gdn_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("ld", ctypes.c_int64), ("hd", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class gdn_rope_params(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("orig_ctx", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("mscale", ctypes.c_double)]
+
+
+class gdn_rope_table(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("axis_end", ctypes.c_int32 * 4), ("mscale", ctypes.c_float), ("turns", ctypes.c_double * 128)]
+
+
+class gdn_kv(ctypes.Structure):
+    _fields_ = [("n_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("format", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class gdn_kv_batch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("start", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int32), ("n_batch", ctypes.c_int32), ("n_tok", ctypes.c_int32)]
 
 
 GDN_GRAPH_VERIFY = 0x1
@@ -94,10 +127,19 @@ def lib() -> ctypes.CDLL:
         L.gdn_graph_launch.argtypes = [P, P]
         L.gdn_linear.argtypes = [P, P, I, I, I, ctypes.POINTER(gdn_out_seg), I, P]
         L.gdn_graph_destroy.argtypes = [P]
+        R, T = ctypes.POINTER(gdn_rows), ctypes.POINTER(gdn_rope_table)
+        K, B = ctypes.POINTER(gdn_kv), ctypes.POINTER(gdn_kv_batch)
+        L.gdn_rope_init.argtypes = [ctypes.POINTER(gdn_rope_params), T]
+        L.gdn_rope.argtypes = [T, R, R, I, I, P, I, I, P]
+        L.gdn_kv_bytes.argtypes = [K, ctypes.POINTER(S)]
+        L.gdn_kv_bytes.restype = S
+        L.gdn_kv_write.argtypes = [K, B, R, R, T, P, P]
+        L.gdn_kv_read.argtypes = [K, B, R, R, P]
+        L.gdn_kv_commit.argtypes = [K, B, P, P, I, P]
         for f in ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_batch",
                   "gdn_rollback_trim", "gdn_prefill", "gdn_prefill_noalloc", "gdn_reset", "gdn_snapshot", "gdn_restore",
                   "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch", "gdn_graph_destroy",
-                  "gdn_linear"):
+                  "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_write", "gdn_kv_read", "gdn_kv_commit"):
             getattr(L, f).restype = ctypes.c_int
         L.gdn_last_error.restype = ctypes.c_char_p
         L.gdn_version.restype = ctypes.c_char_p
@@ -270,3 +312,145 @@ def gdn_snapshot(dims, state, conv_state, snap_state, snap_conv, slots, n: int, 
 def gdn_restore(dims, state, conv_state, snap_state, snap_conv, slots, n: int, stream=None) -> None:
     _check(lib().gdn_restore(ctypes.byref(dims), _p(state), _p(conv_state), _p(snap_state), _p(snap_conv),
                              _p(slots), n, _stream(stream)))
+
+
+# ---- the full-attention layers: rotary positions, the paged KV cache, attention ----
+
+def _bad(msg: str) -> GdnError:
+    return GdnError(GDN_ERR_ARG, msg)
+
+
+def _on_device(fn: str, *tensors) -> None:
+    """The tensors' memory is on the current device: the launch goes there."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != here):
+            raise _bad(f"{fn}: a tensor is on {t.device}, not on the current device cuda:{here}")
+
+
+def _ints(fn: str, name: str, t, *shape):
+    """A contiguous int32 tensor of at least the wanted shape (leading sizes may be larger)."""
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise _bad(f"{fn}: {name} must be a contiguous int32 tensor")
+    if t.dim() != len(shape) or t.shape[1:] != tuple(shape[1:]) or t.shape[0] < shape[0]:
+        raise _bad(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    return t.data_ptr()
+
+
+def _rows(fn: str, name: str, t, n_rows: int, d: int) -> gdn_rows:
+    """gdn_rows of a [n_rows][n_heads][d] tensor whose channels are contiguous (other strides are free)."""
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise GdnError(GDN_ERR_DTYPE, f"{fn}: {name} must be bfloat16 or float32, not {t.dtype}")
+    if t.dim() != 3 or t.shape[0] < n_rows or t.shape[2] != d or (d > 1 and t.stride(2) != 1):
+        raise _bad(f"{fn}: {name} must be [{n_rows}][heads][{d}] with contiguous channels, got {tuple(t.shape)} "
+                   f"with strides {t.stride()}")
+    # a single row or head may carry any stride in torch; it is never stepped over
+    ld = t.stride(0) if t.shape[0] > 1 else 0
+    hd = t.stride(1) if t.shape[1] > 1 else 0
+    return gdn_rows(t.data_ptr(), ld, hd, t.shape[1], GDN_BF16 if t.dtype == torch.bfloat16 else GDN_F32)
+
+
+def gdn_rope_init(rot_dim: int, *, theta: float = 1e4, layout: int = GDN_ROPE_HALF, scaling: int = GDN_ROPE_PLAIN,
+                  factor: float = 1.0, orig_ctx: int = 0, sections=None, beta_fast: float = 0.0,
+                  beta_slow: float = 0.0, mscale: float = 0.0) -> gdn_rope_table:
+    """The rotary table of the parameters (host memory, kept by the caller)."""
+    sec = (ctypes.c_int32 * 4)(*(list(sections) + [0, 0, 0, 0])[:4]) if sections else (ctypes.c_int32 * 4)()
+    p = gdn_rope_params(rot_dim, layout, scaling, orig_ctx, sec, theta, factor, beta_fast, beta_slow, mscale)
+    t = gdn_rope_table()
+    _check(lib().gdn_rope_init(ctypes.byref(p), ctypes.byref(t)))
+    return t
+
+
+def gdn_rope(table: gdn_rope_table, segs, positions, n_tok: int, *, inverse: bool = False, stream=None) -> None:
+    """Rotate segs, a list of (x, out) tensors [n_tok][heads][d] (out may be x); positions int32
+    [n_axes][n_tok]."""
+    d = segs[0][0].shape[-1] if segs else 0
+    for x, out in segs:
+        _on_device("gdn_rope", x, out)
+    _on_device("gdn_rope", positions)
+    xs = (gdn_rows * len(segs))(*[_rows("gdn_rope", "x", x, n_tok, d) for x, _ in segs])
+    outs = (gdn_rows * len(segs))(*[_rows("gdn_rope", "out", o, n_tok, d) for _, o in segs])
+    _check(lib().gdn_rope(ctypes.byref(table), xs, outs, len(segs), d,
+                          _ints("gdn_rope", "positions", positions, table.n_axes, n_tok), n_tok, int(bool(inverse)),
+                          _stream(stream)))
+
+
+class KvCache:
+    """A layer's paged KV cache over caller-owned tensors: k and v [n_pages][n_kv][page_size][d] in
+    bfloat16, float8_e4m3fn or int8, the 8-bit ones with fp32 k_scale and v_scale [n_pages][n_kv][page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, *, flags: int = 0):
+        import torch
+        formats = {torch.bfloat16: GDN_KV_BF16, torch.float8_e4m3fn: GDN_KV_E4M3, torch.int8: GDN_KV_I8}
+        if k.dtype not in formats or v.dtype != k.dtype:
+            raise GdnError(GDN_ERR_DTYPE, f"KvCache: k and v must both be one of {list(formats)}")
+        scales = [s for s in (k_scale, v_scale) if s is not None]
+        if k.dim() != 4 or v.shape != k.shape or any(s.shape != k.shape[:3] or s.dtype != torch.float32 for s in scales):
+            raise _bad("KvCache: k and v are [n_pages][n_kv][page_size][d], scales their first three sizes in float32")
+        if not all(t.is_contiguous() for t in (k, v, *scales)):
+            raise _bad("KvCache: the cache's tensors must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        n_pages, n_kv, page_size, d = k.shape
+        self.c = gdn_kv(n_kv, d, page_size, n_pages, formats[k.dtype], flags, _p(k), _p(v), _p(k_scale), _p(v_scale))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    def _here(self, fn: str) -> None:
+        _on_device(fn, self.k, self.v, self.k_scale, self.v_scale)
+
+
+def gdn_kv_bytes(n_kv: int, d: int, page_size: int, n_pages: int, fmt: int) -> tuple:
+    """(bytes of k, bytes of k_scale) of a cache of these sizes; v takes as much again."""
+    kv = gdn_kv(n_kv, d, page_size, n_pages, fmt, 0, None, None, None, None)
+    sb = ctypes.c_size_t(0)
+    return lib().gdn_kv_bytes(ctypes.byref(kv), ctypes.byref(sb)), sb.value
+
+
+def _batch(fn: str, block_table, start, n_new, n_batch: int, n_tok: int) -> gdn_kv_batch:
+    _on_device(fn, block_table, start, n_new)
+    wide = block_table.shape[1] if block_table.dim() == 2 else 0
+    return gdn_kv_batch(_ints(fn, "block_table", block_table, n_batch, wide), _ints(fn, "start", start, n_batch),
+                        None if n_new is None else _ints(fn, "n_new", n_new, n_batch), wide, n_batch, n_tok)
+
+
+def gdn_kv_write(kv: KvCache, k, v, block_table, start, n_new, n_batch: int, n_tok: int, *,
+                 rope: Optional[gdn_rope_table] = None, positions=None, stream=None) -> None:
+    """k and v [n_batch * n_tok][n_kv][d] into the cache at positions start[b] + t, k rotated by ``rope`` on the
+    way; positions int32 [n_axes][n_batch * n_tok]."""
+    fn, n = "gdn_kv_write", n_batch * n_tok
+    kv._here(fn)
+    _on_device(fn, k, v, positions)
+    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
+    kr, vr = _rows(fn, "k", k, n, kv.c.d), _rows(fn, "v", v, n, kv.c.d)
+    if rope is not None and positions is None:
+        raise _bad("gdn_kv_write: rope needs positions")
+    pos = _ints(fn, "positions", positions, rope.n_axes, n) if rope is not None else None
+    _check(lib().gdn_kv_write(kv.ref, ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr),
+                              ctypes.byref(rope) if rope is not None else None, pos, _stream(stream)))
+
+
+def gdn_kv_read(kv: KvCache, block_table, start, n_new, k, v, n_batch: int, n_tok: int, *, stream=None) -> None:
+    """Positions start[b] + t of the cache into k and v [n_batch * n_tok][n_kv][d]."""
+    fn, n = "gdn_kv_read", n_batch * n_tok
+    kv._here(fn)
+    _on_device(fn, k, v)
+    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
+    kr, vr = _rows(fn, "k", k, n, kv.c.d), _rows(fn, "v", v, n, kv.c.d)
+    _check(lib().gdn_kv_read(kv.ref, ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), _stream(stream)))
+
+
+def gdn_kv_commit(kv: KvCache, block_table, start, path, n_path, n_batch: int, n_tok: int, *, n_new=None,
+                  stream=None) -> None:
+    """Move the cache rows of the accepted nodes path[b][:n_path[b]] (of n_tok per entry) to start[b], start[b] + 1, ..."""
+    fn = "gdn_kv_commit"
+    kv._here(fn)
+    _on_device(fn, path, n_path)
+    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
+    wide = path.shape[1] if path.dim() == 2 else 0
+    _check(lib().gdn_kv_commit(kv.ref, ctypes.byref(b), _ints(fn, "path", path, n_batch, wide),
+                               _ints(fn, "n_path", n_path, n_batch), wide, _stream(stream)))

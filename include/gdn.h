@@ -394,6 +394,153 @@ typedef struct gdn_out_seg {
 int gdn_linear(const void *x, const void *w, int32_t M, int32_t N, int32_t K, const gdn_out_seg *segs,
                int32_t n_segs, void *stream);
 
+/*
+ * The full-attention layers of the same step (lucebox-hub internal.h, struct TargetWeights and
+ * struct TargetCache: partial rotary positions by up to four position axes, a KV cache held in
+ * 8 bits and written by rows, attention of the drafted chain or tree): rotary positions, a paged
+ * KV cache, and the attention of the drafted tokens over it.  Shared by these entry points:
+ *
+ * gdn_rows names per-token rows of heads: the d channels of head h of token t start at
+ * ptr + (t * ld + h * hd) elements, contiguous; ld and hd may be any strides, so q, k and v may
+ * stay inside the fused rows that one projection wrote.
+ */
+typedef struct gdn_rows {
+    void *ptr;
+    int64_t ld;      /* elements from one token to the next */
+    int64_t hd;      /* elements from one head to the next */
+    int32_t n_heads;
+    int32_t dtype;   /* GDN_F32 or GDN_BF16 */
+} gdn_rows;
+
+/* Which channels form the pair of frequency i, i < rot_dim / 2. */
+enum gdn_rope_layout {
+    GDN_ROPE_HALF = 0,       /* channels i and i + rot_dim / 2 */
+    GDN_ROPE_INTERLEAVED = 1 /* channels 2 i and 2 i + 1 */
+};
+/* How the frequencies theta^(-2 i / rot_dim) are changed for contexts longer than the trained one. */
+enum gdn_rope_scaling {
+    GDN_ROPE_PLAIN = 0,  /* not at all */
+    GDN_ROPE_LINEAR = 1, /* every frequency divided by factor */
+    GDN_ROPE_NTK = 2,    /* theta multiplied by factor^(rot_dim / (rot_dim - 2)) */
+    GDN_ROPE_YARN = 3    /* by parts (Peng et al., "YaRN", 2023): pairs that turn over beta_fast times within
+                          * orig_ctx tokens are kept, those under beta_slow times divided by factor, and those
+                          * between blended linearly in i; cos and sin times 0.1 ln(factor) + 1 */
+};
+typedef struct gdn_rope_params {
+    int32_t rot_dim;     /* channels that rotate, from channel 0: even, 2 .. 256 */
+    int32_t layout;      /* gdn_rope_layout */
+    int32_t scaling;     /* gdn_rope_scaling */
+    int32_t orig_ctx;    /* YARN: the trained context length */
+    int32_t sections[4]; /* pairs of each position axis, in order (lucebox-hub internal.h, TargetWeights: rope
+                          * sections 11, 11, 10, 0 over 64 channels); sum rot_dim / 2, or all 0: one axis */
+    double theta;        /* > 1 */
+    double factor;       /* LINEAR, NTK, YARN: >= 1 */
+    double beta_fast, beta_slow; /* YARN; 0, 0 = 32, 1 */
+    double mscale;       /* multiplies cos and sin; 0 = the scaling's own (1; YARN as above) */
+} gdn_rope_params;
+
+#define GDN_ROPE_MAX_PAIRS 128
+/* What gdn_rope_init makes of the parameters: plain host memory, read during the calls that take
+ * it only.  turns[i] is the frequency of pair i in turns per position, frequency / (2 pi). */
+typedef struct gdn_rope_table {
+    int32_t rot_dim, layout, n_axes;
+    int32_t axis_end[4]; /* pairs below axis_end[a] (and not below axis_end[a - 1]) turn with axis a */
+    float mscale;
+    double turns[GDN_ROPE_MAX_PAIRS];
+} gdn_rope_table;
+
+/* Fill *table; host arithmetic in double, no device call.  NULL -> GDN_ERR_ARG; rot_dim odd or
+ * outside 2 .. 256, sections that do not sum to rot_dim / 2 -> GDN_ERR_SHAPE; an unknown layout or
+ * scaling, theta not > 1 and finite, factor < 1, NTK with rot_dim 2, a YARN without orig_ctx >= 1 or
+ * with beta_fast < beta_slow, a negative mscale -> GDN_ERR_ARG. */
+int gdn_rope_init(const gdn_rope_params *params, gdn_rope_table *table);
+
+/*
+ * Rotary positions of n_segs (1 .. 4) sets of rows in one launch (a layer's q and k): for token t,
+ * head h and pair i with channels (a, b) and angle = positions[axis(i)][t] * frequency_i
+ *   out_a = m (x_a cos - x_b sin),  out_b = m (x_a sin + x_b cos),
+ * inverse != 0: by the negative angle, which is also the gradient of the rotation.  Channels from
+ * rot_dim to d are copied.  Angles are formed and reduced in 64 bits, so far positions lose nothing;
+ * the rotation is in 32 bits, rounded once.  positions: device int32 [n_axes][n_tok], any value.
+ * x[s] and out[s]: rows of d channels (rot_dim <= d <= 256) with equal n_heads; in place if they
+ * name the same memory with the same strides and type, otherwise they must not overlap.  Types of x
+ * and out may differ.  n_tok == 0 is a no-op (positions and ptr may then be NULL).  Errors: NULL ->
+ * GDN_ERR_ARG; n_segs, n_heads (1 .. 8192) or d out of range -> GDN_ERR_SHAPE; n_tok < 0 ->
+ * GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE; same pointer with other strides or types, a pointer not
+ * aligned to its elements, a table that gdn_rope_init did not make -> GDN_ERR_ARG.
+ */
+int gdn_rope(const gdn_rope_table *table, const gdn_rows *x, const gdn_rows *out, int32_t n_segs,
+             int32_t d, const int32_t *positions, int32_t n_tok, int32_t inverse, void *stream);
+
+/*
+ * A paged KV cache of one layer (lucebox-hub internal.h, struct TargetCache: attn_k and attn_v,
+ * held in 8 bits).  k and v are [n_pages][n_kv][page_size][d] of the format's elements, 16-byte
+ * aligned; the 8-bit formats keep one fp32 scale per token and head, k_scale and v_scale
+ * [n_pages][n_kv][page_size] (NULL for GDN_KV_BF16): value = code * scale, scale = max |x| / 448
+ * (e4m3) or / 127 (i8), code = x * (1 / scale) rounded to nearest, ties to even.  A row of zeros has
+ * scale 0.  A row that holds an infinity or a NaN gets codes 0 and scale NaN, so that every value of
+ * it reads back as NaN.  flags: GDN_F_CHECK_INDICES or 0.
+ */
+enum gdn_kv_format { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1, GDN_KV_I8 = 2 };
+typedef struct gdn_kv {
+    int32_t n_kv;      /* KV heads */
+    int32_t d;         /* head dim: 64, 128 or 256 */
+    int32_t page_size; /* tokens per page: a power of two, 16 .. 4096 */
+    int32_t n_pages;   /* pages in the pool */
+    int32_t format;    /* gdn_kv_format */
+    uint32_t flags;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} gdn_kv;
+
+/* Bytes of kv->k (and of kv->v) for the struct's sizes and format; *scale_bytes (if not NULL) those
+ * of kv->k_scale.  0 on invalid sizes; the pointers are not looked at. */
+size_t gdn_kv_bytes(const gdn_kv *kv, size_t *scale_bytes);
+
+/*
+ * The tokens of a call: n_tok for each of n_batch entries (row b * n_tok + t of the call's rows is
+ * token t of entry b), of which the first n_new[b] (device int32, NULL = n_tok; taken as at most
+ * n_tok) count.  Token t of entry b has position start[b] + t in the entry's own run of pages:
+ * position p lies at place p mod page_size of page block_table[b][p / page_size] (device int32
+ * [n_batch][max_pages]).  An entry with start[b] < 0 is skipped, and so is a position past the table or
+ * whose page is outside [0, n_pages): nothing is read or written there; rows of tokens that do not count
+ * are left as they were.  With GDN_F_CHECK_INDICES in kv->flags the host copies the arrays back
+ * (synchronously) and returns GDN_ERR_RANGE for any of these before launching; on a capturing
+ * stream that is GDN_ERR_ARG.  n_batch 1 .. 65535, n_tok >= 1.
+ */
+typedef struct gdn_kv_batch {
+    const int32_t *block_table;
+    const int32_t *start;
+    const int32_t *n_new;
+    int32_t max_pages, n_batch, n_tok;
+} gdn_kv_batch;
+
+/*
+ * Write the tokens' k and v rows into the cache (the pages write KV by rows: lucebox-hub
+ * internal.h, QwenGraphInputs), rounded once to the format.  rope != NULL: k is rotated on the
+ * way as gdn_rope would, by positions (device int32 [n_axes][n_batch * n_tok]; a tree's nodes have
+ * their depth, not their index, in them), without a rounding between.  Two tokens of a call must
+ * not have the same place in the cache.  k, v: rows of kv->n_kv heads of kv->d channels, equal dtype,
+ * 16-byte aligned with strides that keep that alignment.
+ * Errors: NULL, misaligned rows, scales missing or given for the wrong format -> GDN_ERR_ARG; sizes,
+ * n_heads, rope->rot_dim > d -> GDN_ERR_SHAPE; unknown dtype or format -> GDN_ERR_DTYPE.
+ */
+int gdn_kv_write(const gdn_kv *kv, const gdn_kv_batch *batch, const gdn_rows *k, const gdn_rows *v,
+                 const gdn_rope_table *rope, const int32_t *positions, void *stream);
+/* Read the tokens' k and v back from the cache into rows of either dtype (the mirror of
+ * gdn_kv_write, without the rotation).  Errors as gdn_kv_write. */
+int gdn_kv_read(const gdn_kv *kv, const gdn_kv_batch *batch, const gdn_rows *k, const gdn_rows *v,
+                void *stream);
+/*
+ * Keep the accepted path of a verified tree (what gdn_rollback does for the GDN layers): for each
+ * entry the cache rows of nodes path[b][0 .. n_path[b]) (device int32 [n_batch][max_path], strictly
+ * increasing node indices) move to positions start[b], start[b] + 1, ...; codes and scales are
+ * copied bit for bit.  n_path[b] is taken as at most max_path.  batch->n_tok is the tree's node count;
+ * a path entry that is not a node index, or is below its own place in the path, is skipped.
+ */
+int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *path,
+                  const int32_t *n_path, int32_t max_path, void *stream);
+
 /* Thread-local description of the last error of this thread ("" after success).  The pages'
  * header keeps one error-reporting channel that its loaders and graph builders write to, with
  * calls returning failure and leaving the message there (lucebox-hub internal.h, set_last_error);
