@@ -1,0 +1,881 @@
+// gdn_attn.hip - attention of drafted tokens over the paged KV cache (gfx950).
+//
+//   o_r = sum_j w_rj v_j / sum_j w_rj,   w_rj = 2^(s_rj - m_r),   s_rj = log2(e) scale q_r . k_j
+//
+// over the keys j that row r sees, with the running maximum m_r and sum kept per row while the keys
+// pass by once (lucebox-hub internal.h, struct QwenGraphInputs: full attention over the cache for the
+// tokens of a chain or tree).  A row is a (token, query head of the group) pair: the group's query
+// heads share a KV head, so all rows of an entry share the keys, and the rows of all entries share
+// those of a prefix.
+//
+// Work: items are (KV head, tile of rows) with their key tiles in sequence.  A launch's key tiles, all
+// items one after another, are cut into equal runs, one per workgroup, whatever the lengths in the
+// cache are; a workgroup scans the entries' lengths at its start to find its run.  An item cut by a
+// run's end leaves partial results (o, m, l) in the workspace, joined by attn_join_kernel.
+//
+// Tile: a workgroup's NR x NK waves hold 16 RT NR rows; each wave takes BN / NK of the tile's keys.
+// S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: with the keys along the result's rows,
+// a lane's scores, its row's maximum, sum and outputs all belong to query row lane % 16, so the
+// softmax needs two cross-lane steps per tile and P goes from the first product's result registers to
+// the second's operand registers without leaving the lane (the key order inside a 32-deep step is
+// permuted alike on both operands).  K and V lie in LDS as bf16, 8-bit codes converted on the way in
+// (both 8-bit formats are exact in bf16); their scales multiply scores and weights in fp32.  Weights
+// are rounded to bf16 for the second product, as its operands are: 2^-9 of each weight, averaged over
+// the keys, beside the output's own 2^-9.
+#include <algorithm>
+#include <type_traits>
+
+#include "gdn_rows.h"
+
+namespace gdn {
+
+typedef __attribute__((__vector_size__(4 * sizeof(__bf16)))) __bf16 bf16x4_lds;
+typedef unsigned long long u64x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ f4 mfma_kq(bf16x8_t a, bf16x8_t b, f4 c)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+#else
+    (void)a;
+    (void)b;
+    return c;
+#endif
+}
+
+// Transposing LDS load: within 16 lanes, lane i receives element i % 4 of the 4-element chunks that
+// lanes i / 4, i / 4 + 4, i / 4 + 8 and i / 4 + 12 address.
+__device__ __forceinline__ unsigned long long lds_tr4(const unsigned char *p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto lp = (__attribute__((address_space(3))) bf16x4_lds *)(const_cast<unsigned char *>(p));
+    return __builtin_bit_cast(unsigned long long, __builtin_amdgcn_ds_read_tr16_b64_v4bf16(lp));
+#else
+    (void)p;
+    return 0;
+#endif
+}
+
+// Over the four lanes that share lane % 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float quad_max(float x)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+#endif
+    return x;
+}
+__device__ __forceinline__ float quad_sum(float x)
+{
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
+    return x;
+}
+
+// 2^(x - m) with 2^(-inf - -inf) = 0: m is the finite stand-in of soft_max below.
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float finite_max(float m) { return m == kNegInf ? 0.0f : m; }
+
+// Eight 8-bit codes as bf16, exactly.
+template <int FMT>
+__device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi)
+{
+    bf16x8_t v;
+    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        if constexpr (FMT == kKvE4m3) {
+            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, false);
+            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, true);
+            v[4 * q] = a[0];
+            v[4 * q + 1] = a[1];
+            v[4 * q + 2] = b[0];
+            v[4 * q + 3] = b[1];
+        } else
+#endif
+        {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * q + j] = (__bf16)(float)(int8_t)(w[q] >> (8 * j));
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------------- items and runs
+
+struct Item {
+    int entry;         // batch entry (prefix: unused)
+    int row0, rows;    // the tile's first row and the rows there are, among the entry's (prefix: the batch's)
+    int ctx;           // keys below it are seen by every row
+    int limit;         // keys that exist for this item
+    int tiles;
+};
+
+template <bool PREFIX>
+__device__ __forceinline__ Item attn_item(const AttnArgs &a, const AttnPhase &ph, int item)
+{
+    Item it{};
+    if constexpr (PREFIX) {
+        const int *live = reinterpret_cast<const int *>(a.ws + a.plan.live);
+        it.row0 = item * ph.bm;
+        it.rows = (a.b.n_new ? live[0] : a.b.n_batch * a.b.n_tok) * a.grp;
+        const int64_t cap = (int64_t)a.max_prefix_pages << a.kv.shift;
+        it.limit = it.ctx = (int)min((int64_t)max(a.prefix_len[0], 0), cap);
+        it.tiles = it.row0 < it.rows ? (it.limit + ph.bn - 1) / ph.bn : 0;
+    } else {
+        it.entry = item / ph.row_tiles;
+        it.row0 = (item - it.entry * ph.row_tiles) * ph.bm;
+        const int start = a.b.start[it.entry], n = kv_new(a.b, it.entry);
+        it.rows = n * a.grp;
+        if (start < 0 || it.row0 >= it.rows) return it;
+        // a chain's last row of the tile sees no key after its own token
+        const int last = a.parent ? n - 1 : (min(it.row0 + ph.bm, it.rows) - 1) / a.grp;
+        const int64_t cap = (int64_t)a.b.max_pages << a.kv.shift;
+        it.ctx = (int)min((int64_t)start, cap);
+        it.limit = (int)min((int64_t)start + last + 1, cap);
+        it.tiles = (it.limit + ph.bn - 1) / ph.bn;
+    }
+    return it;
+}
+
+// ------------------------------------------------------------------------------------ the tile kernel
+
+template <int D, int FMT, int NR, int NK, int RT, int BN_, int OCC>
+struct AttnTile {
+    static constexpr int THREADS = 64 * NR * NK, BM = 16 * RT * NR, BN = BN_, KW = BN / NK, KB = KW / 16;
+    static constexpr int ROWB = D * 2;                           // bytes of a row in LDS
+    static constexpr int ES = FMT == kKvBf16 ? 2 : 1, CPR = D * ES / 16;  // 16-byte chunks of a cache row
+    static constexpr int NCH = BN * CPR / THREADS;               // chunks of K (and of V) per thread
+    static constexpr int SWZ = (D / 8 < 16 ? D / 8 : 16) - 1;
+    static constexpr int kv_bytes = 2 * BN * ROWB, merge_bytes = NK > 1 ? BM * D * 4 : 0;
+    static constexpr int tile_bytes = kv_bytes > merge_bytes ? kv_bytes : merge_bytes;
+    // K, V (reused to join the waves' outputs) | k scales | v scales | bad | good blocks | scan | m, l
+    static constexpr int o_ks = tile_bytes, o_vs = o_ks + BN * 4, o_bad = o_vs + BN * 4, o_ok = o_bad + 16,
+                         o_scan = o_ok + 32, o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
+    static_assert(KW % 32 == 0 && NCH >= 1 && BN * CPR % THREADS == 0 && BN <= 128 && 2 * BN <= THREADS, "tile");
+    static_assert(64 / CPR <= 16, "a wave's chunks of one pass lie in one 16-row block");
+};
+
+template <int D, int FMT, int NR, int NK, int RT, int BN, int OCC, bool PREFIX>
+__global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
+{
+    using TL = AttnTile<D, FMT, NR, NK, RT, BN, OCC>;
+    constexpr int THREADS = TL::THREADS, BM = TL::BM, KW = TL::KW, KB = TL::KB, NCH = TL::NCH, CPR = TL::CPR;
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    unsigned char *kl = lds, *vl = lds + BN * TL::ROWB;
+    float *ksc = reinterpret_cast<float *>(lds + TL::o_ks), *vsc = reinterpret_cast<float *>(lds + TL::o_vs);
+    int *bad = reinterpret_cast<int *>(lds + TL::o_bad);  // v of the item's tiles held something not finite
+   
+    int *good = reinterpret_cast<int *>(lds + TL::o_ok), *scan = reinterpret_cast<int *>(lds + TL::o_scan);
+    float *ml = reinterpret_cast<float *>(lds + TL::o_ml);
+    const AttnPhase &ph = PREFIX ? a.plan.prefix : a.plan.suffix;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lg = lane >> 4, wr = wave / NK, wk = wave % NK;
+    // Workgroups are dealt to the 8 XCDs in turn; neighbouring runs, which may share keys, go to one XCD.
+    const int W = gridDim.x;
+    const int wg = W % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8) * (W / 8) + (int)(blockIdx.x / 8);
+
+    // ---- this workgroup's run of key tiles
+    const int chunk = (ph.items + THREADS - 1) / THREADS;
+    int mine = 0;
+    for (int i = tid * chunk; i < min((tid + 1) * chunk, ph.items); ++i) mine += attn_item<PREFIX>(a, ph, i).tiles;
+    int upto = mine;  // inclusive scan: waves, then across them
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) {
+        const int v = __shfl_up(upto, m);
+        if (lane >= m) upto += v;
+    }
+    if (lane == 63) scan[wave] = upto;
+    __syncthreads();
+    int before = upto - mine, total_head = 0;
+#pragma unroll
+    for (int w = 0; w < NR * NK; ++w) {
+        const int v = scan[w];
+        if (w < wave) before += v;
+        total_head += v;
+    }
+    const uint32_t total = (uint32_t)total_head * (uint32_t)a.kv.n_kv;
+    const uint32_t per = max(1u, (total + W - 1) / W);
+    if (wg == 0 && tid == 0) *reinterpret_cast<uint32_t *>(a.ws + ph.per) = per;
+    uint32_t unit = per * (uint32_t)wg;
+    const uint32_t end = min(unit + per, total);
+    if (unit >= end) return;
+    int head = (int)(unit / (uint32_t)total_head), item = 0, off = 0;
+    {
+        const int rem = (int)(unit - (uint32_t)head * (uint32_t)total_head);
+        if (rem >= before && rem < before + mine) {
+            int i = tid * chunk, left = rem - before;
+            for (;; ++i) {
+                const int t = attn_item<PREFIX>(a, ph, i).tiles;
+                if (left < t) break;
+                left -= t;
+            }
+            scan[THREADS] = i;
+            scan[THREADS + 1] = left;
+        }
+        __syncthreads();
+        item = __builtin_amdgcn_readfirstlane(scan[THREADS]);
+        off = __builtin_amdgcn_readfirstlane(scan[THREADS + 1]);
+    }
+
+    while (unit < end) {
+        const Item it = attn_item<PREFIX>(a, ph, item);
+        const int kt0 = off, kt1 = min(it.tiles, off + (int)(end - unit));
+        if (it.tiles > 0) {
+            if (kt0 == 0 && tid == 0)
+                reinterpret_cast<uint32_t *>(a.ws + ph.first)[head * ph.items + item] = unit;
+            const int *table = PREFIX ? a.prefix_pages : a.b.table + (int64_t)it.entry * a.b.max_pages;
+
+            // ---- staging: this thread's chunks of a tile travel in registers a tile ahead, the pages
+            // they lie on two tiles ahead.  A wave's rows of one pass lie in one aligned run of at most
+            // 16, so on one page: its address is uniform but for the lane's fixed offset.  Every load
+            // is made: a page that is not in the pool becomes page 0, rows past the limit are there
+            // with the page they end, and neither is seen by any query row.
+            u32x4_t kreg[NCH], vreg[NCH];
+            int pg[NCH];
+            uint32_t there = 0;  // bit i: pass i's page is in the pool
+            float sreg = 0.0f;
+            int spg = -1;
+            const int in_page = (1 << a.kv.shift) - 1;
+            const auto page_at = [&](int pos) { return pos < it.limit ? table[pos >> a.kv.shift] : -1; };
+            const auto pass_row = [&](int i) { return (64 * wave + THREADS * i) / CPR; };
+            const int srow = tid % BN;  // 8-bit formats: thread's row of the k (tid < BN) or v scales
+            const auto fetch_pages = [&](int kt) {
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) pg[i] = page_at(kt * BN + pass_row(i));
+                if (FMT != kKvBf16 && tid < 2 * BN) spg = page_at(kt * BN + srow);
+            };
+            const auto row_of = [&](int page, int pos) {
+                return (((int64_t)page * a.kv.n_kv + head) << a.kv.shift) + (pos & in_page);
+            };
+            const auto issue = [&](int kt) {
+                there = 0;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    const bool in_pool = (uint32_t)pg[i] < (uint32_t)a.kv.n_pages;
+                    there |= (uint32_t)in_pool << i;
+                    const int64_t at = row_of(in_pool ? pg[i] : 0, kt * BN + pass_row(i)) * (D * TL::ES);
+                    kreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.k + at + 16 * lane);
+                    vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
+                }
+                if (FMT != kKvBf16 && tid < 2 * BN) {
+                    const bool in_pool = (uint32_t)spg < (uint32_t)a.kv.n_pages;
+                    sreg = (tid < BN ? a.kv.ks : a.kv.vs)[row_of(in_pool ? spg : 0, kt * BN + srow)];
+                    if (!in_pool) sreg = 0.0f;
+                }
+            };
+            // Registers to LDS.  guard: the tile holds keys from ctx on, which some row may not see.
+            // What is not finite in their v must not meet a zero weight: it becomes 0 here, and the
+            // item's end adds it for the rows that do see it.
+            const auto put = [&](int kt, bool guard) {
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    const int row = pass_row(i) + lane / CPR, c = lane % CPR, z = row & TL::SWZ;
+                    if (c == 0 && (row & 15) == 0) good[row >> 4] = (there >> i) & 1;
+                    bf16x8_t kk[2], vv[2];
+                    if constexpr (FMT == kKvBf16) {
+                        kk[0] = __builtin_bit_cast(bf16x8_t, kreg[i]);
+                        vv[0] = __builtin_bit_cast(bf16x8_t, vreg[i]);
+                    } else {
+                        kk[0] = widen8<FMT>(kreg[i][0], kreg[i][1]);
+                        kk[1] = widen8<FMT>(kreg[i][2], kreg[i][3]);
+                        vv[0] = widen8<FMT>(vreg[i][0], vreg[i][1]);
+                        vv[1] = widen8<FMT>(vreg[i][2], vreg[i][3]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2 / TL::ES; ++e) {
+                        if (!((there >> i) & 1)) vv[e] = bf16x8_t{};
+                        if (FMT != kKvI8 && guard && kt * BN + row >= it.ctx) {
+                            bool any = false;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const bool off = (__builtin_bit_cast(uint16_t, (__bf16)vv[e][j]) & 0x7f80) == 0x7f80;
+                                any |= off;
+                                if (off) vv[e][j] = (__bf16)0.0f;
+                            }
+                            if (any) *bad = 1;
+                        }
+                        const int cc = FMT == kKvBf16 ? c : 2 * c + e;
+                        const int at = row * TL::ROWB + ((cc ^ z) * 16);
+                        *reinterpret_cast<bf16x8_t *>(kl + at) = kk[e];
+                        *reinterpret_cast<bf16x8_t *>(vl + at) = vv[e];
+                    }
+                }
+                if (FMT != kKvBf16 && tid < 2 * BN) {
+                    if (guard && tid >= BN && kt * BN + srow >= it.ctx && !(__builtin_fabsf(sreg) < __builtin_inff())) {
+                        sreg = 0.0f;
+                        *bad = 1;
+                    }
+                    (tid < BN ? ksc : vsc)[srow] = sreg;
+                }
+            };
+            fetch_pages(kt0);
+
+            // ---- the tile's query rows: B operand, lane li holds row li of each 16-row block
+            bf16x8_t qf[RT][D / 32];
+            int tok[RT];  // token of the row within its entry; -1 past the last row
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int r = it.row0 + 16 * (RT * wr + rt) + li;
+                tok[rt] = -1;
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks) qf[rt][ks] = bf16x8_t{};
+                if (r < it.rows) {
+                    const int t = r / a.grp, g = r - t * a.grp;
+                    tok[rt] = t;
+                    int64_t row = PREFIX ? t : (int64_t)it.entry * a.b.n_tok + t;
+                    if (PREFIX && a.b.n_new) row = reinterpret_cast<const int *>(a.ws + a.plan.live)[1 + t];
+                    const __bf16 *q = static_cast<const __bf16 *>(a.q.p) + row * a.q.ld + (int64_t)(head * a.grp + g) * a.q.hd;
+#pragma unroll
+                    for (int ks = 0; ks < D / 32; ++ks)
+                        qf[rt][ks] = *reinterpret_cast<const bf16x8_t *>(q + 32 * ks + 8 * lg);
+                }
+            }
+            f4 o[RT][D / 16];
+            float m[RT], l[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                m[rt] = kNegInf;
+                l[rt] = 0.0f;
+#pragma unroll
+                for (int cb = 0; cb < D / 16; ++cb) o[rt][cb] = f4{0.f, 0.f, 0.f, 0.f};
+            }
+
+            // A row sees the positions below seen[rt]: the context and, in a chain, itself and what was
+            // drafted before it; the rest of a tree's row is in its ancestor words.
+            int seen[RT];
+            const uint32_t *anc[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                seen[rt] = PREFIX ? it.limit : min(it.limit, it.ctx + (a.parent ? 0 : tok[rt] + 1));
+                anc[rt] = reinterpret_cast<const uint32_t *>(a.ws + a.plan.anc) +
+                          ((int64_t)it.entry * a.b.n_tok + max(tok[rt], 0)) * a.plan.words;
+            }
+            const auto in_tree = [&](const uint32_t *words, int pos) {  // ctx <= pos < limit
+                const int rel = pos - it.ctx;
+                return ((words[rel >> 5] >> (rel & 31)) & 1) != 0;
+            };
+            const auto compute = [&](int kt, bool masked) {
+                f4 s[RT][KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) s[rt][kb] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        // row 16 kb + li of the wave's keys: its swizzle is li's alone
+                        const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(
+                            kl + (wk * KW + 16 * kb + li) * TL::ROWB + (((4 * ks + lg) ^ (li & TL::SWZ)) * 16));
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) s[rt][kb] = mfma_kq(kf, qf[rt][ks], s[rt][kb]);
+                    }
+                }
+                float top[RT];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) top[rt] = kNegInf;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const int k0 = wk * KW + 16 * kb + 4 * lg;  // the lane's four keys of the block
+                    f4 c = f4{a.scale, a.scale, a.scale, a.scale};
+                    if constexpr (FMT != kKvBf16) {
+                        const f4 ks = *reinterpret_cast<const f4 *>(ksc + k0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] *= ks[i];
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[rt][kb][i] *= c[i];
+                }
+                if (masked) {
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        const bool there = good[(wk * KW >> 4) + kb] != 0;
+                        const int p0 = kt * BN + wk * KW + 16 * kb + 4 * lg;
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                bool on = p0 + i < seen[rt];
+                                if (!PREFIX && a.parent && !on && p0 + i < it.limit) on = in_tree(anc[rt], p0 + i);
+                                s[rt][kb][i] = on && there ? s[rt][kb][i] : kNegInf;
+                            }
+                    }
+                }
+                bool grew = false;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[rt][kb][i]);
+                    top[rt] = quad_max(top[rt]);
+                    grew |= top[rt] > m[rt];
+                }
+                if (__any(grew)) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float mn = fmaxf(m[rt], top[rt]), f = exp2_f(m[rt] - finite_max(mn));
+                        m[rt] = mn;
+                        l[rt] *= f;
+#pragma unroll
+                        for (int cb = 0; cb < D / 16; ++cb)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[rt][cb][i] *= f;
+                    }
+                }
+                bf16x8_t pf[RT][KB / 2];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    f4 vs = f4{1.f, 1.f, 1.f, 1.f};
+                    if constexpr (FMT != kKvBf16) vs = *reinterpret_cast<const f4 *>(vsc + wk * KW + 16 * kb + 4 * lg);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float p = exp2_f(s[rt][kb][i] - finite_max(m[rt]));
+                            l[rt] += p;
+                            if constexpr (FMT != kKvBf16) p *= vs[i];
+                            pf[rt][kb / 2][4 * (kb % 2) + i] = (__bf16)p;
+                        }
+                }
+#pragma unroll
+                for (int kp = 0; kp < KB / 2; ++kp) {
+                    const int r = 4 * lg + (li >> 2), z = r & TL::SWZ;  // row 32 kp + r, then 16 rows on
+                    const unsigned char *base = vl + (wk * KW + 32 * kp + r) * TL::ROWB + (li & 1) * 8;
+#pragma unroll
+                    for (int cb = 0; cb < D / 16; ++cb) {
+                        const int c = ((2 * cb + ((li & 3) >> 1)) ^ z) * 16;
+                        const bf16x8_t vf =
+                            __builtin_bit_cast(bf16x8_t, u64x2_t{lds_tr4(base + c), lds_tr4(base + c + 16 * TL::ROWB)});
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) o[rt][cb] = mfma_kq(vf, pf[rt][kp], o[rt][cb]);
+                    }
+                }
+            };
+
+            if (tid == 0) *bad = 0;  // before the loop's first barrier
+            issue(kt0);
+            if (kt0 + 1 < kt1) fetch_pages(kt0 + 1);
+#pragma unroll 1
+            for (int kt = kt0; kt < kt1; ++kt) {
+                const bool tail = (kt + 1) * BN > it.ctx;  // keys that some row may not see
+                __syncthreads();                           // the last tile's reads are done
+                put(kt, tail);
+                __syncthreads();
+                if (kt + 1 < kt1) {
+                    issue(kt + 1);
+                    if (kt + 2 < kt1) fetch_pages(kt + 2);
+                }
+                int all = 1;
+#pragma unroll
+                for (int i = 0; i < BN / 16; ++i) all &= good[i];
+                compute(kt, tail || !__builtin_amdgcn_readfirstlane(all));
+            }
+
+            // ---- join the key waves: the last one ends with the item's sums
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) l[rt] = quad_sum(l[rt]);
+            if constexpr (NK > 1) {
+                __syncthreads();  // tile reads done: its LDS is free
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    if (lg == 0) ml[wk * BM + 16 * (RT * wr + rt) + li] = m[rt];
+                __syncthreads();
+                float *ob = reinterpret_cast<float *>(lds);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int r = 16 * (RT * wr + rt) + li;
+                    float mn = kNegInf;
+#pragma unroll
+                    for (int w = 0; w < NK; ++w) mn = fmaxf(mn, ml[w * BM + r]);
+                    const float f = exp2_f(m[rt] - finite_max(mn));
+                    m[rt] = mn;
+                    l[rt] *= f;
+#pragma unroll
+                    for (int cb = 0; cb < D / 16; ++cb)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[rt][cb][i] *= f;
+                }
+                __syncthreads();  // maxima read: ml now carries the sums
+                for (int w = 0; w < NK; ++w) {
+                    if (wk == w) {
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const int r = 16 * (RT * wr + rt) + li;
+                            if (w > 0) l[rt] += ml[r];
+#pragma unroll
+                            for (int cb = 0; cb < D / 16; ++cb) {
+                                f4 *at = reinterpret_cast<f4 *>(ob + r * D + ((4 * cb + lg) ^ (r & 15)) * 4);
+                                if (w > 0) o[rt][cb] += *at;
+                                if (w + 1 < NK) *at = o[rt][cb];
+                            }
+                        }
+                        if (w + 1 < NK)
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt)
+                                if (lg == 0) ml[16 * (RT * wr + rt) + li] = l[rt];
+                    }
+                    __syncthreads();
+                }
+            }
+            if (wk == NK - 1) {
+                // What put() took out of v, for the rows that see it: infinities and NaNs add up to what
+                // they are whatever their weight.
+                if (__builtin_amdgcn_readfirstlane(*bad)) {
+#pragma unroll 1
+                    for (int pos = max(it.ctx, kt0 * BN); pos < min(it.limit, kt1 * BN); ++pos) {
+                        const int page = page_at(pos);
+                        if ((uint32_t)page >= (uint32_t)a.kv.n_pages) continue;
+                        const int64_t at = row_of(page, pos);
+                        const bool none = FMT != kKvBf16 && !(__builtin_fabsf(a.kv.vs[at]) < __builtin_inff());
+#pragma unroll
+                        for (int cb = 0; cb < D / 16; ++cb) {
+                            const int64_t ch = at * D + 16 * cb + 4 * lg;
+                            float x[4];
+                            if constexpr (FMT == kKvBf16) {
+                                load_row<4>(a.kv.v, ch, true, x);
+                            } else {
+                                const uint32_t w = *reinterpret_cast<const uint32_t *>(a.kv.v + ch);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    x[e] = none || (FMT == kKvE4m3 && ((w >> (8 * e)) & 0x7f) == 0x7f) ? __builtin_nanf("") : 0.0f;
+                            }
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                bool on = pos < seen[rt];
+                                if (!PREFIX && a.parent && !on) on = in_tree(anc[rt], pos);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (on && !(__builtin_fabsf(x[e]) < __builtin_inff())) o[rt][cb][e] += x[e];
+                            }
+                        }
+                    }
+                }
+                const bool final = !PREFIX && !a.prefix_pages && kt0 == 0 && kt1 == it.tiles;
+                const int64_t slot = (int64_t)head * ph.items + item + wg;  // its own: item and wg never both go back
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int lr = 16 * (RT * wr + rt) + li, r = it.row0 + lr;
+                    if (r >= it.rows) continue;
+                    if (final) {
+                        const int t = r / a.grp, g = r - t * a.grp;
+                        const float inv = l[rt] == 0.0f ? 0.0f : 1.0f / l[rt];
+                        __bf16 *out = static_cast<__bf16 *>(a.out.p) + ((int64_t)it.entry * a.b.n_tok + t) * a.out.ld +
+                                      (int64_t)(head * a.grp + g) * a.out.hd;
+#pragma unroll
+                        for (int cb = 0; cb < D / 16; ++cb) {
+                            bf16x4_t y;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) y[i] = (__bf16)(o[rt][cb][i] * inv);
+                            *reinterpret_cast<bf16x4_t *>(out + 16 * cb + 4 * lg) = y;
+                        }
+                    } else {
+                        float *po = reinterpret_cast<float *>(a.ws + ph.po) + (slot * BM + lr) * D;
+#pragma unroll
+                        for (int cb = 0; cb < D / 16; ++cb) *reinterpret_cast<f4 *>(po + 16 * cb + 4 * lg) = o[rt][cb];
+                        if (lg == 0) reinterpret_cast<float2 *>(a.ws + ph.pml)[slot * BM + lr] = make_float2(m[rt], l[rt]);
+                    }
+                }
+            }
+            __syncthreads();  // LDS is free for the next item
+        }
+        unit += kt1 - kt0;
+        off = 0;
+        if (++item == ph.items) {
+            item = 0;
+            ++head;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------- before and after
+
+// Bit j of node t's words: node t sees drafted node j, its ancestor or itself.
+__global__ __launch_bounds__(256) void attn_ancestors_kernel(AttnArgs a)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)a.b.n_batch * a.b.n_tok) return;
+    const int64_t b = i / a.b.n_tok;
+    const int32_t *parent = a.parent + b * a.b.n_tok;
+    uint32_t *w = reinterpret_cast<uint32_t *>(a.ws + a.plan.anc) + i * a.plan.words;
+    int node = (int)(i - b * a.b.n_tok), up = 0;
+    for (int word = a.plan.words - 1; word >= 0; --word) {
+        uint32_t bits = 0;
+        while (node >= 32 * word) {  // a parent comes before its child, so the walk ends
+            bits |= 1u << (node & 31);
+            up = parent[node];
+            node = up < node ? up : -1;
+            if (node < 0) node = -1;
+            if (node < 0) break;
+        }
+        w[word] = bits;
+    }
+}
+
+// The token rows that count, in order, and each one's place among them: live[0] is their number.
+__global__ __launch_bounds__(1024) void attn_live_kernel(AttnArgs a)
+{
+    __shared__ int part[16];
+    __shared__ int base;
+    int *live = reinterpret_cast<int *>(a.ws + a.plan.live), *rank = reinterpret_cast<int *>(a.ws + a.plan.rank);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = a.b.n_batch * a.b.n_tok;
+    if (tid == 0) base = 0;
+    for (int i0 = 0; i0 < n; i0 += 1024) {
+        const int i = i0 + tid, b = i / a.b.n_tok;
+        const bool on = i < n && a.b.start[b] >= 0 && i - b * a.b.n_tok < kv_new(a.b, b);
+        const uint64_t vote = __ballot(on);
+        if (lane == 0) part[wave] = __popcll(vote);
+        __syncthreads();
+        int at = base;
+        for (int w = 0; w < wave; ++w) at += part[w];
+        at += __popcll(vote & ((1ull << lane) - 1));
+        if (on) {
+            live[1 + at] = i;
+            rank[i] = at;
+        }
+        __syncthreads();
+        if (tid == 1023) base = at + on;
+    }
+    __syncthreads();
+    if (tid == 0) live[0] = base;
+}
+
+// The parts of one item: slots [slot, slot + n).
+struct Parts {
+    int64_t slot;
+    int n, row;
+};
+template <bool PREFIX>
+__device__ __forceinline__ Parts attn_parts(const AttnArgs &a, const AttnPhase &ph, int item, int row, int head)
+{
+    const Item it = attn_item<PREFIX>(a, ph, item);
+    if (it.tiles <= 0) return Parts{0, 0, 0};
+    const uint32_t per = *reinterpret_cast<const uint32_t *>(a.ws + ph.per);
+    const uint32_t u = reinterpret_cast<const uint32_t *>(a.ws + ph.first)[head * ph.items + item];
+    const uint32_t w0 = u / per, w1 = (u + it.tiles - 1) / per;
+    return Parts{(int64_t)head * ph.items + item + w0, (int)(w1 - w0 + 1), row - it.row0};
+}
+
+// One row of the result from its parts: WPR waves share a row (many parts: few rows with long
+// contexts), the block's other waves take other rows.
+template <int D, int WPR>
+__global__ __launch_bounds__(512) void attn_join_kernel(AttnArgs a)
+{
+    constexpr int E = D / 64, ROWS = 8 / WPR;
+    __shared__ float so[8][D];
+    __shared__ float2 sml[8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % WPR;
+    const int n_q = a.kv.n_kv * a.grp;
+    const int64_t id = (int64_t)blockIdx.x * ROWS + wave / WPR;
+    const int64_t tokrow = id / n_q;
+    const int hq = (int)(id - tokrow * n_q), head = hq / a.grp, g = hq - head * a.grp;
+    const int b = (int)(tokrow / a.b.n_tok), t = (int)(tokrow - (int64_t)b * a.b.n_tok);
+    bool work = tokrow < (int64_t)a.b.n_batch * a.b.n_tok && a.b.start[min(b, a.b.n_batch - 1)] >= 0 &&
+                t < kv_new(a.b, min(b, a.b.n_batch - 1));
+    Parts own{0, 0, 0}, pre{0, 0, 0};
+    if (work) {
+        const AttnPhase &sp = a.plan.suffix, &pp = a.plan.prefix;
+        int r = t * a.grp + g;
+        own = attn_parts<false>(a, sp, b * sp.row_tiles + r / sp.bm, r, head);
+        if (a.prefix_pages) {
+            const int at = a.b.n_new ? reinterpret_cast<const int *>(a.ws + a.plan.rank)[tokrow] : (int)tokrow;
+            r = at * a.grp + g;
+            pre = attn_parts<true>(a, pp, r / pp.bm, r, head);
+        } else if (own.n == 1) {
+            work = false;  // written whole
+        }
+    }
+    float m = kNegInf, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    if (work) {
+        const auto take = [&](const AttnPhase &ph, const Parts &p) {
+            const float *po = reinterpret_cast<const float *>(a.ws + ph.po);
+            const float2 *pml = reinterpret_cast<const float2 *>(a.ws + ph.pml);
+            constexpr int U = 8;  // parts in flight
+            for (int j0 = sub; j0 < p.n; j0 += WPR * U) {
+                float x[U][E];
+                float2 y[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    y[u] = make_float2(kNegInf, 0.0f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
+                    const int j = j0 + WPR * u;
+                    if (j >= p.n) continue;
+                    const int64_t at = (p.slot + j) * ph.bm + p.row;
+                    y[u] = pml[at];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[u][e] = po[at * D + E * lane + e];
+                }
+                float mn = m;
+#pragma unroll
+                for (int u = 0; u < U; ++u) mn = fmaxf(mn, y[u].x);
+                const float f = exp2_f(m - finite_max(mn));
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float w = exp2_f(y[u].x - finite_max(mn));
+                    l += w * y[u].y;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] += w * x[u][e];
+                }
+                m = mn;
+            }
+        };
+        if (a.prefix_pages) take(a.plan.prefix, pre);
+        take(a.plan.suffix, own);
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[wave][E * lane + e] = o[e];
+        if (lane == 0) sml[wave] = make_float2(m, l);
+        __syncthreads();
+        if (sub != 0) return;
+        float mn = kNegInf;
+        for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, sml[wave + w].x);
+        l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.0f;
+        for (int w = 0; w < WPR; ++w) {
+            const float f = exp2_f(sml[wave + w].x - finite_max(mn));
+            l += f * sml[wave + w].y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] += f * so[wave + w][E * lane + e];
+        }
+    }
+    if (!work) return;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __bf16 *out = static_cast<__bf16 *>(a.out.p) + tokrow * a.out.ld + (int64_t)hq * a.out.hd + E * lane;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = (__bf16)(o[e] * inv);
+}
+
+// -------------------------------------------------------------------------------------- launches
+
+// Tile shapes by the rows that share keys: 16 or 32 rows with the keys of a 128-key tile dealt to four
+// waves, 64 rows on 2 x 2 waves, 128 rows on four waves.
+static int attn_config(int64_t rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+constexpr int kAttnBm[4] = {16, 32, 64, 128}, kAttnBn[4] = {128, 128, 64, 64};
+
+bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch, int n_tok, int max_pages, bool prefix,
+               int max_prefix_pages, AttnPlan &p)
+{
+    (void)format;
+    p = AttnPlan{};
+    const int cus = 256, per_cu = d == 256 ? 1 : 2;
+    size_t at = 0;
+    const auto room = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    bool fits = true;
+    const auto phase = [&](AttnPhase &ph, int64_t rows, int entries, int64_t pages) {
+        ph.cfg = attn_config(rows);
+        ph.bm = kAttnBm[ph.cfg];
+        ph.bn = kAttnBn[ph.cfg];
+        const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
+        const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
+        if (items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
+            (double)items * n_kv * (double)tiles >= 2147483648.0) {
+            fits = false;
+            return;
+        }
+        ph.row_tiles = (int)row_tiles;
+        ph.items = (int)items;
+        ph.wgs = (int)std::min<int64_t>(cus * per_cu, items * n_kv * tiles);
+        const size_t slots = (size_t)(items * n_kv) + cus * per_cu;
+        ph.per = room(4);
+        ph.first = room((size_t)(items * n_kv) * 4);
+        ph.pml = room(slots * ph.bm * 8);
+        ph.po = room(slots * ph.bm * d * 4);
+    };
+    phase(p.suffix, (int64_t)n_tok * grp, n_batch, max_pages);
+    if (prefix && fits) {
+        phase(p.prefix, (int64_t)n_batch * n_tok * grp, 1, max_prefix_pages);
+        p.live = room(((size_t)n_batch * n_tok + 1) * 4);
+        p.rank = room((size_t)n_batch * n_tok * 4);
+    }
+    p.words = (n_tok + 31) / 32;
+    if (n_tok <= 1024) p.anc = room((size_t)n_batch * n_tok * p.words * 4);  // the longest tree
+    p.bytes = at;
+    return fits;
+}
+
+template <int D, int FMT, int NR, int NK, int RT, int BN, int OCC, bool PREFIX>
+static hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream)
+{
+    using TL = AttnTile<D, FMT, NR, NK, RT, BN, OCC>;
+    const AttnPhase &ph = PREFIX ? a.plan.prefix : a.plan.suffix;
+    hipLaunchKernelGGL((attn_kernel<D, FMT, NR, NK, RT, BN, OCC, PREFIX>), dim3(ph.wgs), dim3(TL::THREADS), TL::lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int D, int FMT, bool PREFIX>
+static hipError_t launch_cfg(const AttnArgs &a, hipStream_t stream)
+{
+    constexpr int OCC = D == 256 ? 1 : 2;  // waves per SIMD that the registers must allow
+    switch ((PREFIX ? a.plan.prefix : a.plan.suffix).cfg) {
+    case 0: return launch_tiles<D, FMT, 1, 4, 1, 128, OCC, PREFIX>(a, stream);
+    case 1: return launch_tiles<D, FMT, 1, 4, 2, 128, OCC, PREFIX>(a, stream);
+    case 2: return launch_tiles<D, FMT, 2, 2, 2, 64, OCC, PREFIX>(a, stream);
+    default: return launch_tiles<D, FMT, 4, 1, 2, 64, OCC, PREFIX>(a, stream);
+    }
+}
+
+template <int D>
+static hipError_t launch_join(const AttnArgs &a, hipStream_t stream)
+{
+    const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok * a.kv.n_kv * a.grp;
+    // Few rows can have many parts each: a block of eight waves per row while that does not need more
+    // than four blocks per CU, else a wave per row.
+    if (rows <= 1024)
+        hipLaunchKernelGGL((attn_join_kernel<D, 8>), dim3((unsigned)rows), dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)((rows + 7) / 8)), dim3(512), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int D>
+static hipError_t launch_attn_d(const AttnArgs &a, hipStream_t stream)
+{
+    const auto tiles = [&](auto prefix) {
+        constexpr bool P = decltype(prefix)::value;
+        return a.kv.format == kKvBf16   ? launch_cfg<D, kKvBf16, P>(a, stream)
+               : a.kv.format == kKvE4m3 ? launch_cfg<D, kKvE4m3, P>(a, stream)
+                                        : launch_cfg<D, kKvI8, P>(a, stream);
+    };
+    const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok;
+    if (a.parent) {
+        hipLaunchKernelGGL(attn_ancestors_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (a.prefix_pages) {
+        if (a.b.n_new) {
+            hipLaunchKernelGGL(attn_live_kernel, dim3(1), dim3(1024), 0, stream, a);
+            if (hipError_t e = hipGetLastError()) return e;
+        }
+        if (hipError_t e = tiles(std::true_type{})) return e;
+    }
+    if (hipError_t e = tiles(std::false_type{})) return e;
+    // where no item can have a second tile and there is no prefix, every row was written whole
+    if (!a.prefix_pages && ((int64_t)a.b.max_pages << a.kv.shift) <= a.plan.suffix.bn) return hipSuccess;
+    return launch_join<D>(a, stream);
+}
+
+hipError_t launch_attn(const AttnArgs &a, hipStream_t stream)
+{
+    return a.kv.d == 64 ? launch_attn_d<64>(a, stream) : a.kv.d == 128 ? launch_attn_d<128>(a, stream) : launch_attn_d<256>(a, stream);
+}
+
+}  // namespace gdn

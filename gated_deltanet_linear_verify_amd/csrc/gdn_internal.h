@@ -175,6 +175,38 @@ struct KvCommitArgs {
     int32_t max_path;
 };
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t stream);
+// Attention of drafted tokens (gdn_attn.hip).  A launch's work is a list of items, each a tile of query
+// rows of one KV head with the keys they see; AttnPhase describes one launch's items.
+struct AttnPhase {
+    int32_t cfg;        // tile shape, by rows (attn_config)
+    int32_t bm, bn;     // rows and keys of a tile
+    int32_t row_tiles;  // row tiles per entry (the prefix: of the whole batch)
+    int32_t items;      // items per KV head
+    int32_t wgs;        // workgroups launched
+    size_t po, pml, first, per;  // workspace offsets: partial outputs, their (max, sum), first units, units per workgroup
+};
+struct AttnPlan {
+    AttnPhase suffix, prefix;
+    size_t live, rank, anc, bytes;  // workspace offsets: token rows that count, their places, ancestor words
+    int32_t words;                  // ancestor words per node
+};
+struct AttnArgs {
+    KvView kv;
+    KvBatchView b;
+    RowsView q, out;
+    int32_t grp;                    // query heads per KV head
+    float scale;                    // of the scores, times log2(e)
+    const int32_t *parent;          // tree, else NULL
+    const int32_t *prefix_pages, *prefix_len;
+    int32_t max_prefix_pages;
+    unsigned char *ws;
+    AttnPlan plan;
+};
+// Sizes only; false where a launch's tiles would pass 2^31.
+bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch, int n_tok, int max_pages, bool prefix,
+               int max_prefix_pages, AttnPlan &p);
+hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
+
 // Checks shared by the cache's entry points (gdn_kv_abi.cpp); each sets the last error.
 int abi_check_kv(const char *fn, const gdn_kv *kv, bool pointers);
 int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_heads);  // aligned rows

@@ -28,7 +28,7 @@ EXPORTS = ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback",
            "gdn_prefill", "gdn_prefill_noalloc", "gdn_prefill_workspace_bytes", "gdn_capture_bytes", "gdn_reset",
            "gdn_snapshot", "gdn_restore", "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch",
            "gdn_graph_destroy", "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_bytes", "gdn_kv_write",
-           "gdn_kv_read", "gdn_kv_commit", "gdn_last_error", "gdn_version")
+           "gdn_kv_read", "gdn_kv_commit", "gdn_attn_verify", "gdn_attn_workspace_bytes", "gdn_last_error", "gdn_version")
 
 
 class GdnError(RuntimeError):
@@ -136,10 +136,14 @@ def lib() -> ctypes.CDLL:
         L.gdn_kv_write.argtypes = [K, B, R, R, T, P, P]
         L.gdn_kv_read.argtypes = [K, B, R, R, P]
         L.gdn_kv_commit.argtypes = [K, B, P, P, I, P]
+        L.gdn_attn_verify.argtypes = [K, B, P, P, I, P, R, R, ctypes.c_float, P, S, P]
+        L.gdn_attn_workspace_bytes.argtypes = [K, I, I, I, I]
+        L.gdn_attn_workspace_bytes.restype = S
         for f in ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_batch",
                   "gdn_rollback_trim", "gdn_prefill", "gdn_prefill_noalloc", "gdn_reset", "gdn_snapshot", "gdn_restore",
                   "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch", "gdn_graph_destroy",
-                  "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_write", "gdn_kv_read", "gdn_kv_commit"):
+                  "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_write", "gdn_kv_read", "gdn_kv_commit",
+                  "gdn_attn_verify"):
             getattr(L, f).restype = ctypes.c_int
         L.gdn_last_error.restype = ctypes.c_char_p
         L.gdn_version.restype = ctypes.c_char_p
@@ -454,3 +458,24 @@ def gdn_kv_commit(kv: KvCache, block_table, start, path, n_path, n_batch: int, n
     wide = path.shape[1] if path.dim() == 2 else 0
     _check(lib().gdn_kv_commit(kv.ref, ctypes.byref(b), _ints(fn, "path", path, n_batch, wide),
                                _ints(fn, "n_path", n_path, n_batch), wide, _stream(stream)))
+
+
+def gdn_attn_workspace_bytes(kv: KvCache, n_q: int, n_batch: int, n_tok: int, prefix: bool = False) -> int:
+    return lib().gdn_attn_workspace_bytes(kv.ref, n_q, n_batch, n_tok, int(bool(prefix)))
+
+
+def gdn_attn_verify(kv: KvCache, q, block_table, start, n_new, parent, prefix_pages, prefix_len, out, n_batch: int,
+                    n_tok: int, scale: float, workspace, *, stream=None) -> None:
+    """Attention of q [n_batch * n_tok][n_q][d] over the cache into out, a chain (parent None) or a tree, with an
+    optional prefix shared by the batch: prefix_pages int32 [pages], prefix_len int32 [1]."""
+    fn, n = "gdn_attn_verify", n_batch * n_tok
+    kv._here(fn)
+    _on_device(fn, q, out, parent, prefix_pages, prefix_len, workspace)
+    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
+    qr, outr = _rows(fn, "q", q, n, kv.c.d), _rows(fn, "out", out, n, kv.c.d)
+    par = None if parent is None else _ints(fn, "parent", parent, n_batch, n_tok)
+    pre = None if prefix_pages is None else _ints(fn, "prefix_pages", prefix_pages, 1)
+    plen = None if prefix_len is None else _ints(fn, "prefix_len", prefix_len, 1)
+    _check(lib().gdn_attn_verify(kv.ref, ctypes.byref(b), par, pre, 0 if pre is None else prefix_pages.shape[0], plen,
+                                 ctypes.byref(qr), ctypes.byref(outr), scale, workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))

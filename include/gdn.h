@@ -541,6 +541,35 @@ int gdn_kv_read(const gdn_kv *kv, const gdn_kv_batch *batch, const gdn_rows *k, 
 int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *path,
                   const int32_t *n_path, int32_t max_path, void *stream);
 
+/*
+ * Attention of the drafted tokens (q, already rotated) over the cache, after gdn_kv_write has put
+ * their own k and v there.  Token t of entry b sees, of its entry's positions, the context
+ * [0, start[b]) and of the drafted ones itself and those before it (parent == NULL) or itself and its
+ * ancestors (parent: device int32 [n_batch][n_tok] as in gdn_verify_tree, n_tok <= 1024; malformed
+ * parents count as -1).  prefix_pages != NULL: every entry of the batch also sees the first
+ * prefix_len[0] positions (device int32, taken as at most max_prefix_pages * page_size) of the run of
+ * pages prefix_pages (device int32 [max_prefix_pages]): a prefix that all share, held once, and
+ * scored for the rows of all entries together, so its pages are read once for the batch.
+ *   out = sum_j softmax_j(scale q . k_j) v_j,  query head h reading KV head h / (n_q / n_kv).
+ * Scores, maxima and sums are in fp32, the weights are rounded to bf16 for the product with v.  A
+ * key that a row does not see does not reach it, whatever its k and v hold.  A row whose keys are
+ * all on pages outside the pool is zero.
+ *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
+ *   gdn_kv_write.  scale: finite, > 0.
+ *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
+ *   calls (and recorded graphs) that may run at the same time need one each.
+ * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, or a bad scale ->
+ * GDN_ERR_ARG; sizes whose tiles would pass 2^31 -> GDN_ERR_SHAPE.
+ */
+int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *parent,
+                    const int32_t *prefix_pages, int32_t max_prefix_pages, const int32_t *prefix_len,
+                    const gdn_rows *q, const gdn_rows *out, float scale, void *workspace,
+                    size_t ws_bytes, void *stream);
+/* Workspace bytes of a gdn_attn_verify call with these sizes (prefix: whether it has one); 0 on
+ * invalid sizes.  It does not depend on the lengths in the cache. */
+size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n_batch, int32_t n_tok,
+                                int32_t prefix);
+
 /* Thread-local description of the last error of this thread ("" after success).  The pages'
  * header keeps one error-reporting channel that its loaders and graph builders write to, with
  * calls returning failure and leaving the message there (lucebox-hub internal.h, set_last_error);

@@ -133,3 +133,35 @@ def test_kv_bytes(L):
     assert gdn.gdn_kv_bytes(8, 128, 64, 1000, gdn.GDN_KV_E4M3) == (8 * 128 * 64 * 1000, 4 * 8 * 64 * 1000)
     assert gdn.gdn_kv_bytes(2, 256, 16, 1 << 20, gdn.GDN_KV_BF16) == (2 * 256 * 16 * 2 << 20, 0)
     assert gdn.gdn_kv_bytes(2, 100, 16, 3, gdn.GDN_KV_BF16) == (0, 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(kv=None), gdn.GDN_ERR_ARG), (dict(batch=None), gdn.GDN_ERR_ARG), (dict(q=None), gdn.GDN_ERR_ARG),
+    (dict(out=None), gdn.GDN_ERR_ARG), (dict(q=_rows(n_heads=6)), gdn.GDN_ERR_SHAPE), (dict(q=_rows(n_heads=2)), gdn.GDN_ERR_SHAPE),
+    (dict(out=_rows(n_heads=8)), gdn.GDN_ERR_SHAPE), (dict(q=_rows(dtype=gdn.GDN_F32)), gdn.GDN_ERR_DTYPE),
+    (dict(out=_rows(dtype=gdn.GDN_F32)), gdn.GDN_ERR_DTYPE), (dict(q=_rows(ptr=FAKE + 2)), gdn.GDN_ERR_ARG),
+    (dict(scale=0.0), gdn.GDN_ERR_ARG), (dict(scale=float("nan")), gdn.GDN_ERR_ARG), (dict(scale=float("inf")), gdn.GDN_ERR_ARG),
+    (dict(parent=FAKE, batch=_batch(n_tok=1025)), gdn.GDN_ERR_SHAPE), (dict(pages=FAKE), gdn.GDN_ERR_ARG),
+    (dict(plen=FAKE), gdn.GDN_ERR_ARG), (dict(pages=FAKE, plen=FAKE, n_pages=0), gdn.GDN_ERR_SHAPE),
+    (dict(ws=None), gdn.GDN_ERR_ARG), (dict(ws=FAKE + 4), gdn.GDN_ERR_ARG), (dict(ws_bytes=100), gdn.GDN_ERR_ARG),
+    (dict(batch=_batch(max_pages=1 << 25)), gdn.GDN_ERR_SHAPE),
+])
+def test_attn_refuses(L, kw, code):
+    a = dict(kv=_kv(), batch=_batch(), parent=None, pages=None, n_pages=3, plen=None, q=_rows(), out=_rows(), scale=0.1,
+             ws=FAKE, ws_bytes=1 << 40)
+    a.update(kw)
+    ref_ = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    assert L.gdn_attn_verify(ref_(a["kv"]), ref_(a["batch"]), a["parent"], a["pages"], a["n_pages"], a["plen"], ref_(a["q"]),
+                             ref_(a["out"]), a["scale"], a["ws"], a["ws_bytes"], None) == code, gdn.last_error()
+
+
+def test_attn_refuses_bad_caches_and_batches(L):
+    r = ctypes.byref(_rows())
+    for kv, b, code in [(_kv(**x), _batch(), c) for x, c in KV_BAD] + [(_kv(), _batch(**x), c) for x, c in BATCH_BAD]:
+        assert L.gdn_attn_verify(ctypes.byref(kv), ctypes.byref(b), None, None, 0, None, r, r, 0.1, FAKE, 1 << 40, None) == code
+
+
+def test_attn_workspace(L):
+    n = lambda n_q, b, t, p, **kw: L.gdn_attn_workspace_bytes(ctypes.byref(_kv(**kw)), n_q, b, t, p)  # noqa: E731
+    assert 0 < n(32, 64, 16, 0) < n(32, 64, 16, 1)
+    assert n(6, 1, 1, 0) == n(32, 0, 1, 0) == n(32, 1, 0, 0) == n(32, 70000, 1, 0) == n(32, 1, 1, 0, d=96) == 0
