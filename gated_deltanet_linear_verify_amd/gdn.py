@@ -182,6 +182,35 @@ def _stream(stream) -> Optional[int]:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+class _Torch:
+    """What the bindings below need of torch for every call, looked up once: a call of a small kernel is
+    bound by the host, and torch.cuda.current_stream() alone builds a Stream object in 2.9 us where the
+    handle is a query of 0.1 us."""
+
+    def __init__(self):
+        import torch
+        torch.cuda.current_device()  # initialises the runtime, or says why it cannot
+        self.dtypes = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+        self.int32 = torch.int32
+        self.device = torch.cuda.current_device
+        self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def stream(self, stream, here: int):
+        if stream is None and self.stream_of is not None:
+            return self.stream_of(here)
+        return _stream(stream)
+
+
+_torch_state = None
+
+
+def _torch() -> _Torch:
+    global _torch_state
+    if _torch_state is None:
+        _torch_state = _Torch()
+    return _torch_state
+
+
 class Capture:
     """Per-position capture buffers (torch tensors) plus the restore targets."""
 
@@ -324,37 +353,35 @@ def _bad(msg: str) -> GdnError:
     return GdnError(GDN_ERR_ARG, msg)
 
 
-def _on_device(fn: str, *tensors) -> None:
-    """The tensors' memory is on the current device: the launch goes there."""
-    import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != here):
-            raise _bad(f"{fn}: a tensor is on {t.device}, not on the current device cuda:{here}")
+def _elsewhere(fn: str, t, here: int) -> GdnError:
+    return _bad(f"{fn}: a tensor is on {t.device}, not on the current device cuda:{here}, where the launch goes")
 
 
-def _ints(fn: str, name: str, t, *shape):
-    """A contiguous int32 tensor of at least the wanted shape (leading sizes may be larger)."""
-    import torch
-    if t.dtype != torch.int32 or not t.is_contiguous():
+def _ints(fn: str, name: str, t, here: int, T: _Torch, n0: int, n1: int = -1) -> int:
+    """Address of a contiguous int32 tensor [n0] or [n0][n1] (the first size may be larger)."""
+    if t.get_device() != here:
+        raise _elsewhere(fn, t, here)
+    if t.dtype is not T.int32 or not t.is_contiguous():
         raise _bad(f"{fn}: {name} must be a contiguous int32 tensor")
-    if t.dim() != len(shape) or t.shape[1:] != tuple(shape[1:]) or t.shape[0] < shape[0]:
-        raise _bad(f"{fn}: {name} has shape {tuple(t.shape)}, expected {shape}")
+    shape = t.shape
+    if len(shape) != (1 if n1 < 0 else 2) or shape[0] < n0 or (n1 >= 0 and shape[1] != n1):
+        raise _bad(f"{fn}: {name} has shape {tuple(shape)}, expected {(n0,) if n1 < 0 else (n0, n1)}")
     return t.data_ptr()
 
 
-def _rows(fn: str, name: str, t, n_rows: int, d: int) -> gdn_rows:
+def _rows(fn: str, name: str, t, here: int, T: _Torch, n_rows: int, d: int) -> gdn_rows:
     """gdn_rows of a [n_rows][n_heads][d] tensor whose channels are contiguous (other strides are free)."""
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    if t.get_device() != here:
+        raise _elsewhere(fn, t, here)
+    dtype = T.dtypes.get(t.dtype)
+    if dtype is None:
         raise GdnError(GDN_ERR_DTYPE, f"{fn}: {name} must be bfloat16 or float32, not {t.dtype}")
-    if t.dim() != 3 or t.shape[0] < n_rows or t.shape[2] != d or (d > 1 and t.stride(2) != 1):
-        raise _bad(f"{fn}: {name} must be [{n_rows}][heads][{d}] with contiguous channels, got {tuple(t.shape)} "
-                   f"with strides {t.stride()}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < n_rows or shape[2] != d or (strides[2] != 1 and d > 1):
+        raise _bad(f"{fn}: {name} must be [{n_rows}][heads][{d}] with contiguous channels, got {tuple(shape)} "
+                   f"with strides {strides}")
     # a single row or head may carry any stride in torch; it is never stepped over
-    ld = t.stride(0) if t.shape[0] > 1 else 0
-    hd = t.stride(1) if t.shape[1] > 1 else 0
-    return gdn_rows(t.data_ptr(), ld, hd, t.shape[1], GDN_BF16 if t.dtype == torch.bfloat16 else GDN_F32)
+    return gdn_rows(t.data_ptr(), strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0, shape[1], dtype)
 
 
 def gdn_rope_init(rot_dim: int, *, theta: float = 1e4, layout: int = GDN_ROPE_HALF, scaling: int = GDN_ROPE_PLAIN,
@@ -371,15 +398,16 @@ def gdn_rope_init(rot_dim: int, *, theta: float = 1e4, layout: int = GDN_ROPE_HA
 def gdn_rope(table: gdn_rope_table, segs, positions, n_tok: int, *, inverse: bool = False, stream=None) -> None:
     """Rotate segs, a list of (x, out) tensors [n_tok][heads][d] (out may be x); positions int32
     [n_axes][n_tok]."""
-    d = segs[0][0].shape[-1] if segs else 0
-    for x, out in segs:
-        _on_device("gdn_rope", x, out)
-    _on_device("gdn_rope", positions)
-    xs = (gdn_rows * len(segs))(*[_rows("gdn_rope", "x", x, n_tok, d) for x, _ in segs])
-    outs = (gdn_rows * len(segs))(*[_rows("gdn_rope", "out", o, n_tok, d) for _, o in segs])
-    _check(lib().gdn_rope(ctypes.byref(table), xs, outs, len(segs), d,
-                          _ints("gdn_rope", "positions", positions, table.n_axes, n_tok), n_tok, int(bool(inverse)),
-                          _stream(stream)))
+    fn, T, n = "gdn_rope", _torch(), len(segs)
+    here = T.device()
+    if not n:
+        raise GdnError(GDN_ERR_SHAPE, "gdn_rope: no rows given")
+    d = segs[0][0].shape[-1]
+    xs, outs = (gdn_rows * n)(), (gdn_rows * n)()
+    for i, (x, out) in enumerate(segs):
+        xs[i], outs[i] = _rows(fn, "x", x, here, T, n_tok, d), _rows(fn, "out", out, here, T, n_tok, d)
+    _check(lib().gdn_rope(table, xs, outs, n, d, _ints(fn, "positions", positions, here, T, table.n_axes, n_tok), n_tok,
+                          1 if inverse else 0, T.stream(stream, here)))
 
 
 class KvCache:
@@ -391,12 +419,13 @@ class KvCache:
         formats = {torch.bfloat16: GDN_KV_BF16, torch.float8_e4m3fn: GDN_KV_E4M3, torch.int8: GDN_KV_I8}
         if k.dtype not in formats or v.dtype != k.dtype:
             raise GdnError(GDN_ERR_DTYPE, f"KvCache: k and v must both be one of {list(formats)}")
-        scales = [s for s in (k_scale, v_scale) if s is not None]
-        if k.dim() != 4 or v.shape != k.shape or any(s.shape != k.shape[:3] or s.dtype != torch.float32 for s in scales):
+        tensors = [t for t in (k, v, k_scale, v_scale) if t is not None]
+        if k.dim() != 4 or v.shape != k.shape or any(s.shape != k.shape[:3] or s.dtype != torch.float32 for s in tensors[2:]):
             raise _bad("KvCache: k and v are [n_pages][n_kv][page_size][d], scales their first three sizes in float32")
-        if not all(t.is_contiguous() for t in (k, v, *scales)):
-            raise _bad("KvCache: the cache's tensors must be contiguous")
+        if not all(t.is_contiguous() for t in tensors) or any(t.device != k.device for t in tensors):
+            raise _bad("KvCache: the cache's tensors must be contiguous and on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.get_device()
         n_pages, n_kv, page_size, d = k.shape
         self.c = gdn_kv(n_kv, d, page_size, n_pages, formats[k.dtype], flags, _p(k), _p(v), _p(k_scale), _p(v_scale))
 
@@ -404,8 +433,12 @@ class KvCache:
     def ref(self):
         return ctypes.byref(self.c)
 
-    def _here(self, fn: str) -> None:
-        _on_device(fn, self.k, self.v, self.k_scale, self.v_scale)
+    def _here(self, fn: str, T: _Torch) -> int:
+        """The current device, which has to hold the cache."""
+        here = T.device()
+        if self.device != here:
+            raise _elsewhere(fn, self.k, here)
+        return here
 
 
 def gdn_kv_bytes(n_kv: int, d: int, page_size: int, n_pages: int, fmt: int) -> tuple:
@@ -415,67 +448,64 @@ def gdn_kv_bytes(n_kv: int, d: int, page_size: int, n_pages: int, fmt: int) -> t
     return lib().gdn_kv_bytes(ctypes.byref(kv), ctypes.byref(sb)), sb.value
 
 
-def _batch(fn: str, block_table, start, n_new, n_batch: int, n_tok: int) -> gdn_kv_batch:
-    _on_device(fn, block_table, start, n_new)
+def _batch(fn: str, here: int, T: _Torch, block_table, start, n_new, n_batch: int, n_tok: int) -> gdn_kv_batch:
     wide = block_table.shape[1] if block_table.dim() == 2 else 0
-    return gdn_kv_batch(_ints(fn, "block_table", block_table, n_batch, wide), _ints(fn, "start", start, n_batch),
-                        None if n_new is None else _ints(fn, "n_new", n_new, n_batch), wide, n_batch, n_tok)
+    return gdn_kv_batch(_ints(fn, "block_table", block_table, here, T, n_batch, wide),
+                        _ints(fn, "start", start, here, T, n_batch),
+                        None if n_new is None else _ints(fn, "n_new", n_new, here, T, n_batch), wide, n_batch, n_tok)
 
 
 def gdn_kv_write(kv: KvCache, k, v, block_table, start, n_new, n_batch: int, n_tok: int, *,
                  rope: Optional[gdn_rope_table] = None, positions=None, stream=None) -> None:
     """k and v [n_batch * n_tok][n_kv][d] into the cache at positions start[b] + t, k rotated by ``rope`` on the
     way; positions int32 [n_axes][n_batch * n_tok]."""
-    fn, n = "gdn_kv_write", n_batch * n_tok
-    kv._here(fn)
-    _on_device(fn, k, v, positions)
-    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
-    kr, vr = _rows(fn, "k", k, n, kv.c.d), _rows(fn, "v", v, n, kv.c.d)
+    fn, T, n, d = "gdn_kv_write", _torch(), n_batch * n_tok, kv.c.d
+    here = kv._here(fn, T)
+    b = _batch(fn, here, T, block_table, start, n_new, n_batch, n_tok)
     if rope is not None and positions is None:
         raise _bad("gdn_kv_write: rope needs positions")
-    pos = _ints(fn, "positions", positions, rope.n_axes, n) if rope is not None else None
-    _check(lib().gdn_kv_write(kv.ref, ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr),
-                              ctypes.byref(rope) if rope is not None else None, pos, _stream(stream)))
+    pos = _ints(fn, "positions", positions, here, T, rope.n_axes, n) if rope is not None else None
+    _check(lib().gdn_kv_write(kv.c, b, _rows(fn, "k", k, here, T, n, d), _rows(fn, "v", v, here, T, n, d), rope, pos,
+                              T.stream(stream, here)))
 
 
 def gdn_kv_read(kv: KvCache, block_table, start, n_new, k, v, n_batch: int, n_tok: int, *, stream=None) -> None:
     """Positions start[b] + t of the cache into k and v [n_batch * n_tok][n_kv][d]."""
-    fn, n = "gdn_kv_read", n_batch * n_tok
-    kv._here(fn)
-    _on_device(fn, k, v)
-    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
-    kr, vr = _rows(fn, "k", k, n, kv.c.d), _rows(fn, "v", v, n, kv.c.d)
-    _check(lib().gdn_kv_read(kv.ref, ctypes.byref(b), ctypes.byref(kr), ctypes.byref(vr), _stream(stream)))
+    fn, T, n, d = "gdn_kv_read", _torch(), n_batch * n_tok, kv.c.d
+    here = kv._here(fn, T)
+    b = _batch(fn, here, T, block_table, start, n_new, n_batch, n_tok)
+    _check(lib().gdn_kv_read(kv.c, b, _rows(fn, "k", k, here, T, n, d), _rows(fn, "v", v, here, T, n, d),
+                             T.stream(stream, here)))
 
 
 def gdn_kv_commit(kv: KvCache, block_table, start, path, n_path, n_batch: int, n_tok: int, *, n_new=None,
                   stream=None) -> None:
     """Move the cache rows of the accepted nodes path[b][:n_path[b]] (of n_tok per entry) to start[b], start[b] + 1, ..."""
-    fn = "gdn_kv_commit"
-    kv._here(fn)
-    _on_device(fn, path, n_path)
-    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
+    fn, T = "gdn_kv_commit", _torch()
+    here = kv._here(fn, T)
+    b = _batch(fn, here, T, block_table, start, n_new, n_batch, n_tok)
     wide = path.shape[1] if path.dim() == 2 else 0
-    _check(lib().gdn_kv_commit(kv.ref, ctypes.byref(b), _ints(fn, "path", path, n_batch, wide),
-                               _ints(fn, "n_path", n_path, n_batch), wide, _stream(stream)))
+    _check(lib().gdn_kv_commit(kv.c, b, _ints(fn, "path", path, here, T, n_batch, wide),
+                               _ints(fn, "n_path", n_path, here, T, n_batch), wide, T.stream(stream, here)))
 
 
 def gdn_attn_workspace_bytes(kv: KvCache, n_q: int, n_batch: int, n_tok: int, prefix: bool = False) -> int:
-    return lib().gdn_attn_workspace_bytes(kv.ref, n_q, n_batch, n_tok, int(bool(prefix)))
+    return lib().gdn_attn_workspace_bytes(kv.c, n_q, n_batch, n_tok, int(bool(prefix)))
 
 
 def gdn_attn_verify(kv: KvCache, q, block_table, start, n_new, parent, prefix_pages, prefix_len, out, n_batch: int,
                     n_tok: int, scale: float, workspace, *, stream=None) -> None:
     """Attention of q [n_batch * n_tok][n_q][d] over the cache into out, a chain (parent None) or a tree, with an
     optional prefix shared by the batch: prefix_pages int32 [pages], prefix_len int32 [1]."""
-    fn, n = "gdn_attn_verify", n_batch * n_tok
-    kv._here(fn)
-    _on_device(fn, q, out, parent, prefix_pages, prefix_len, workspace)
-    b = _batch(fn, block_table, start, n_new, n_batch, n_tok)
-    qr, outr = _rows(fn, "q", q, n, kv.c.d), _rows(fn, "out", out, n, kv.c.d)
-    par = None if parent is None else _ints(fn, "parent", parent, n_batch, n_tok)
-    pre = None if prefix_pages is None else _ints(fn, "prefix_pages", prefix_pages, 1)
-    plen = None if prefix_len is None else _ints(fn, "prefix_len", prefix_len, 1)
-    _check(lib().gdn_attn_verify(kv.ref, ctypes.byref(b), par, pre, 0 if pre is None else prefix_pages.shape[0], plen,
-                                 ctypes.byref(qr), ctypes.byref(outr), scale, workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+    fn, T, n, d = "gdn_attn_verify", _torch(), n_batch * n_tok, kv.c.d
+    here = kv._here(fn, T)
+    b = _batch(fn, here, T, block_table, start, n_new, n_batch, n_tok)
+    par = None if parent is None else _ints(fn, "parent", parent, here, T, n_batch, n_tok)
+    pre = None if prefix_pages is None else _ints(fn, "prefix_pages", prefix_pages, here, T, 1)
+    plen = None if prefix_len is None else _ints(fn, "prefix_len", prefix_len, here, T, 1)
+    if workspace.get_device() != here:
+        raise _elsewhere(fn, workspace, here)
+    _check(lib().gdn_attn_verify(kv.c, b, par, pre, 0 if pre is None else prefix_pages.shape[0], plen,
+                                 _rows(fn, "q", q, here, T, n, d), _rows(fn, "out", out, here, T, n, d), scale,
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 T.stream(stream, here)))
