@@ -14,14 +14,20 @@
 // run's end leaves partial results (o, m, l) in the workspace, joined by attn_join_kernel.
 //
 // Tile: a workgroup's NR x NK waves hold 16 RT NR rows; each wave takes BN / NK of the tile's keys.
-// S^T = K Q^T and O^T = V^T P^T on v_mfma_f32_16x16x32_bf16: with the keys along the result's rows,
-// a lane's scores, its row's maximum, sum and outputs all belong to query row lane % 16, so the
-// softmax needs two cross-lane steps per tile and P goes from the first product's result registers to
-// the second's operand registers without leaving the lane (the key order inside a 32-deep step is
-// permuted alike on both operands).  K and V lie in LDS as bf16, 8-bit codes converted on the way in
-// (both 8-bit formats are exact in bf16); their scales multiply scores and weights in fp32.  Weights
-// are rounded to bf16 for the second product, as its operands are: 2^-9 of each weight, averaged over
-// the keys, beside the output's own 2^-9.
+// S^T = K Q^T and O^T = V^T P^T on 16x16x32 MFMA: with the keys along the result's rows, a lane's
+// scores, its row's maximum, sum and outputs all belong to query row lane % 16, so the softmax needs
+// two cross-lane steps per tile and P goes from the first product's result registers to the second's
+// operand registers without leaving the lane (the key order inside a 32-deep step is permuted alike
+// on both operands).
+//
+// Formats.  A bf16 cache goes into LDS as it is (global_load_lds), its weights are rounded to bf16 for
+// the second product: half a step is 2^-9 .. 2^-8 of a weight, which averages over the keys.  8-bit
+// codes travel through registers and are widened on the way into LDS, k to bf16 and v to fp16, both
+// exactly.  The k scale multiplies the scores; the v scale is folded into the exponent, w_j =
+// 2^(s_j + log2 vs_j - m) with m the maximum of that sum, so the largest weight is 1 whatever the
+// scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's own sum takes w_j / vs_j in
+// fp32.  (That holds while the v scales of the keys a workgroup meets lie within 2^100 of each other;
+// a scale of 0 goes with codes of 0 and counts as 1.)
 #include <algorithm>
 #include <type_traits>
 
@@ -81,30 +87,88 @@ __device__ __forceinline__ float quad_sum(float x)
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float finite_max(float m) { return m == kNegInf ? 0.0f : m; }
 
-// Eight 8-bit codes as bf16, exactly.
-template <int FMT>
-__device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi)
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f4 mfma_vp(bf16x8_t a, bf16x8_t b, f4 c) { return mfma_kq(a, b, c); }
+__device__ __forceinline__ f4 mfma_vp(f16x8_t a, f16x8_t b, f4 c)
 {
-    bf16x8_t v;
+#if defined(__HIP_DEVICE_COMPILE__)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+#else
+    (void)a;
+    (void)b;
+    return c;
+#endif
+}
+
+// Eight 8-bit codes as bf16 (k) or fp16 (v), exactly.
+template <int FMT>
+__device__ __forceinline__ u32x4_t widen_k(uint32_t lo, uint32_t hi)
+{
+    u32x4_t r{};
     const uint32_t w[2] = {lo, hi};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
 #if defined(__HIP_DEVICE_COMPILE__)
         if constexpr (FMT == kKvE4m3) {
-            const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, false);
-            const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, true);
-            v[4 * q] = a[0];
-            v[4 * q + 1] = a[1];
-            v[4 * q + 2] = b[0];
-            v[4 * q + 3] = b[1];
+            r[2 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, false));
+            r[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[q], 1.0f, true));
         } else
 #endif
         {
+            // a whole number of 7 bits and sign: its fp32 ends in 16 zero bits
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * q + j] = (__bf16)(float)(int8_t)(w[q] >> (8 * j));
+            for (int j = 0; j < 2; ++j)
+                r[2 * q + j] = __builtin_amdgcn_perm(__float_as_uint((float)(int8_t)(w[q] >> (16 * j + 8))),
+                                                     __float_as_uint((float)(int8_t)(w[q] >> (16 * j))), 0x07060302u);
         }
     }
-    return v;
+    return r;
+}
+template <int FMT>
+__device__ __forceinline__ u32x4_t widen_v(uint32_t lo, uint32_t hi)
+{
+    u32x4_t r{};
+    const uint32_t w[2] = {lo, hi};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#if defined(__HIP_DEVICE_COMPILE__)
+        if constexpr (FMT == kKvE4m3) {
+            r[2 * q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[q], 1.0f, false));
+            r[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[q], 1.0f, true));
+        } else
+#endif
+        {
+            // code + 128 in the low byte of 0x6400 is 1024 + 128 + code; one subtraction leaves the code
+            const uint32_t u = w[q] ^ 0x80808080u;
+            const f16x2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+            r[2 * q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - bias);
+            r[2 * q + 1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - bias);
+        }
+    }
+    return r;
+}
+
+// What is not finite in 16 bytes of v becomes 0; whether there was any.
+template <int FMT>
+__device__ __forceinline__ bool strip(u32x4_t &v)
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t off = 0;
+        if constexpr (FMT == kKvBf16) {
+            off |= (v[q] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+            off |= (v[q] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+        } else if constexpr (FMT == kKvE4m3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) off |= ((v[q] >> (8 * j)) & 0x7fu) == 0x7fu ? 0xffu << (8 * j) : 0u;
+        }
+        v[q] &= ~off;
+        any |= off;
+    }
+    return any != 0;
 }
 
 // ---------------------------------------------------------------------------------- items and runs
@@ -133,46 +197,57 @@ __device__ __forceinline__ Item attn_item(const AttnArgs &a, const AttnPhase &ph
         it.row0 = (item - it.entry * ph.row_tiles) * ph.bm;
         const int start = a.b.start[it.entry], n = kv_new(a.b, it.entry);
         it.rows = n * a.grp;
-        if (start < 0 || it.row0 >= it.rows) return it;
         // a chain's last row of the tile sees no key after its own token
-        const int last = a.parent ? n - 1 : (min(it.row0 + ph.bm, it.rows) - 1) / a.grp;
+        const int last = a.parent ? n - 1 : (max(min(it.row0 + ph.bm, it.rows), 1) - 1) / a.grp;
         const int64_t cap = (int64_t)a.b.max_pages << a.kv.shift;
-        it.ctx = (int)min((int64_t)start, cap);
-        it.limit = (int)min((int64_t)start + last + 1, cap);
-        it.tiles = (it.limit + ph.bn - 1) / ph.bn;
+        it.ctx = (int)min((int64_t)max(start, 0), cap);
+        it.limit = (int)min((int64_t)max(start, 0) + last + 1, cap);
+        it.tiles = start >= 0 && it.row0 < it.rows ? (it.limit + ph.bn - 1) / ph.bn : 0;
     }
     return it;
 }
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ uint32_t scalar(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+
 // ------------------------------------------------------------------------------------ the tile kernel
 
-template <int D, int FMT, int NR, int NK, int RT, int BN_, int OCC>
+template <int D, int FMT, int NR, int NK, int RT, int BN_, int NB_>
 struct AttnTile {
     static constexpr int THREADS = 64 * NR * NK, BM = 16 * RT * NR, BN = BN_, KW = BN / NK, KB = KW / 16;
+    static constexpr int NB = NB_;                               // buffered tiles
+    static constexpr bool DMA = FMT == kKvBf16;                  // straight into LDS
     static constexpr int ROWB = D * 2;                           // bytes of a row in LDS
-    static constexpr int ES = FMT == kKvBf16 ? 2 : 1, CPR = D * ES / 16;  // 16-byte chunks of a cache row
+    static constexpr int ES = DMA ? 2 : 1, CPR = D * ES / 16;    // 16-byte chunks of a cache row
     static constexpr int NCH = BN * CPR / THREADS;               // chunks of K (and of V) per thread
-    static constexpr int SWZ = (D / 8 < 16 ? D / 8 : 16) - 1;
-    static constexpr int kv_bytes = 2 * BN * ROWB, merge_bytes = NK > 1 ? BM * D * 4 : 0;
-    static constexpr int tile_bytes = kv_bytes > merge_bytes ? kv_bytes : merge_bytes;
-    // K, V (reused to join the waves' outputs) | k scales | v scales | bad | good blocks | scan | m, l
-    static constexpr int o_ks = tile_bytes, o_vs = o_ks + BN * 4, o_bad = o_vs + BN * 4, o_ok = o_bad + 16,
-                         o_scan = o_ok + 32, o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
-    static_assert(KW % 32 == 0 && NCH >= 1 && BN * CPR % THREADS == 0 && BN <= 128 && 2 * BN <= THREADS, "tile");
+    static constexpr int SWZ = (D / 8 < 16 ? D / 8 : 16) - 1;    // chunk c of row r lies at c ^ (r & SWZ)
+    static constexpr int buf_bytes = 2 * BN * ROWB, merge_bytes = NK > 1 ? BM * D * 4 : 0;
+    static constexpr int tile_bytes = NB * buf_bytes > merge_bytes ? NB * buf_bytes : merge_bytes;
+    static constexpr int sc_bytes = DMA ? 0 : 3 * BN * 4;        // k scale | log2 v scale | 1 / v scale
+    // K and V buffers (reused to join the waves' outputs) | scales | good blocks | bad | scan | m, l
+    static constexpr int o_sc = tile_bytes, o_ok = o_sc + NB * sc_bytes, o_bad = o_ok + NB * 32, o_scan = o_bad + 16,
+                         o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
+    static constexpr int waves = NR * NK;
+    // workgroups per CU: by LDS, and eight waves (two per SIMD) where the registers allow that
+    static constexpr int by_lds = 160 * 1024 / lds, occ = D == 256 && RT == 2 && waves == 4 ? 1 : 2;
+    static constexpr int by_waves = 4 * occ / waves, per_cu = by_lds < by_waves ? by_lds : by_waves;
+    static_assert(KW % 32 == 0 && NCH >= 1 && BN * CPR % THREADS == 0 && BN <= 128, "tile");
+    static_assert(DMA ? NB == 2 : 2 * BN <= THREADS, "staging");
     static_assert(64 / CPR <= 16, "a wave's chunks of one pass lie in one 16-row block");
+    static_assert(per_cu >= 1, "one workgroup fits");
 };
 
-template <int D, int FMT, int NR, int NK, int RT, int BN, int OCC, bool PREFIX>
-__global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
+template <int D, int FMT, int NR, int NK, int RT, int BN, int NB, bool PREFIX>
+__global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>::occ)) void attn_kernel(AttnArgs a)
 {
-    using TL = AttnTile<D, FMT, NR, NK, RT, BN, OCC>;
+    using TL = AttnTile<D, FMT, NR, NK, RT, BN, NB>;
     constexpr int THREADS = TL::THREADS, BM = TL::BM, KW = TL::KW, KB = TL::KB, NCH = TL::NCH, CPR = TL::CPR;
+    constexpr bool DMA = TL::DMA;
+    using P8 = std::conditional_t<DMA, bf16x8_t, f16x8_t>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-    unsigned char *kl = lds, *vl = lds + BN * TL::ROWB;
-    float *ksc = reinterpret_cast<float *>(lds + TL::o_ks), *vsc = reinterpret_cast<float *>(lds + TL::o_vs);
     int *bad = reinterpret_cast<int *>(lds + TL::o_bad);  // v of the item's tiles held something not finite
-   
-    int *good = reinterpret_cast<int *>(lds + TL::o_ok), *scan = reinterpret_cast<int *>(lds + TL::o_scan);
+    int *scan = reinterpret_cast<int *>(lds + TL::o_scan);
     float *ml = reinterpret_cast<float *>(lds + TL::o_ml);
     const AttnPhase &ph = PREFIX ? a.plan.prefix : a.plan.suffix;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -181,138 +256,169 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
     const int W = gridDim.x;
     const int wg = W % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8) * (W / 8) + (int)(blockIdx.x / 8);
 
-    // ---- this workgroup's run of key tiles
+    // ---- this workgroup's run of key tiles.  Every loop below runs alike in all lanes and what steers
+    // the kernel is held in scalar registers: values kept in vector registers across lane-dependent
+    // branches have come back wrong from spills that the compiler restored with no lane active.
     const int chunk = (ph.items + THREADS - 1) / THREADS;
     int mine = 0;
-    for (int i = tid * chunk; i < min((tid + 1) * chunk, ph.items); ++i) mine += attn_item<PREFIX>(a, ph, i).tiles;
+    for (int j = 0; j < chunk; ++j) {
+        const int i = tid * chunk + j, t = attn_item<PREFIX>(a, ph, min(i, ph.items - 1)).tiles;
+        mine += i < ph.items ? t : 0;
+    }
     int upto = mine;  // inclusive scan: waves, then across them
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) {
         const int v = __shfl_up(upto, m);
-        if (lane >= m) upto += v;
+        upto += lane >= m ? v : 0;
     }
     if (lane == 63) scan[wave] = upto;
     __syncthreads();
     int before = upto - mine, total_head = 0;
 #pragma unroll
     for (int w = 0; w < NR * NK; ++w) {
-        const int v = scan[w];
+        const int v = __builtin_amdgcn_readfirstlane(scan[w]);
         if (w < wave) before += v;
         total_head += v;
     }
     const uint32_t total = (uint32_t)total_head * (uint32_t)a.kv.n_kv;
     const uint32_t per = max(1u, (total + W - 1) / W);
     if (wg == 0 && tid == 0) *reinterpret_cast<uint32_t *>(a.ws + ph.per) = per;
-    uint32_t unit = per * (uint32_t)wg;
-    const uint32_t end = min(unit + per, total);
+    uint32_t unit = scalar(per * (uint32_t)wg);
+    const uint32_t end = scalar(min(unit + per, total));
     if (unit >= end) return;
-    int head = (int)(unit / (uint32_t)total_head), item = 0, off = 0;
+    int head = scalar(unit / (uint32_t)total_head);
     {
         const int rem = (int)(unit - (uint32_t)head * (uint32_t)total_head);
-        if (rem >= before && rem < before + mine) {
-            int i = tid * chunk, left = rem - before;
-            for (;; ++i) {
-                const int t = attn_item<PREFIX>(a, ph, i).tiles;
-                if (left < t) break;
-                left -= t;
+        for (int j = 0; j < chunk; ++j) {
+            const int i = tid * chunk + j, t = attn_item<PREFIX>(a, ph, min(i, ph.items - 1)).tiles;
+            if (i < ph.items && rem >= before && rem < before + t) {  // one lane of the workgroup, once
+                scan[THREADS] = i;
+                scan[THREADS + 1] = rem - before;
             }
-            scan[THREADS] = i;
-            scan[THREADS + 1] = left;
+            before += t;
         }
         __syncthreads();
-        item = __builtin_amdgcn_readfirstlane(scan[THREADS]);
-        off = __builtin_amdgcn_readfirstlane(scan[THREADS + 1]);
     }
+    int item = scalar(scan[THREADS]), off = scalar(scan[THREADS + 1]);
 
     while (unit < end) {
-        const Item it = attn_item<PREFIX>(a, ph, item);
-        const int kt0 = off, kt1 = min(it.tiles, off + (int)(end - unit));
+        Item it = attn_item<PREFIX>(a, ph, item);
+        it.entry = scalar(it.entry);
+        it.row0 = scalar(it.row0);
+        it.rows = scalar(it.rows);
+        it.ctx = scalar(it.ctx);
+        it.limit = scalar(it.limit);
+        it.tiles = scalar(it.tiles);
+        const int kt0 = off, kt1 = max(kt0, min(it.tiles, off + (int)(end - unit)));
         if (it.tiles > 0) {
             if (kt0 == 0 && tid == 0)
                 reinterpret_cast<uint32_t *>(a.ws + ph.first)[head * ph.items + item] = unit;
             const int *table = PREFIX ? a.prefix_pages : a.b.table + (int64_t)it.entry * a.b.max_pages;
 
-            // ---- staging: this thread's chunks of a tile travel in registers a tile ahead, the pages
-            // they lie on two tiles ahead.  A wave's rows of one pass lie in one aligned run of at most
-            // 16, so on one page: its address is uniform but for the lane's fixed offset.  Every load
-            // is made: a page that is not in the pool becomes page 0, rows past the limit are there
-            // with the page they end, and neither is seen by any query row.
-            u32x4_t kreg[NCH], vreg[NCH];
+            // ---- staging.  The pages a tile lies on are read two tiles ahead, its rows one tile ahead
+            // (bf16: into the other LDS buffer; 8 bits: into registers).  A wave's rows of one pass lie
+            // in one aligned run of at most 16, so on one page: its address is uniform but for the
+            // lane's fixed offset.  Every load is made: a page that is not in the pool becomes page 0, rows
+            // past the limit come from the page that holds its last one, and no query row sees either.
+            u32x4_t kreg[DMA ? 1 : NCH], vreg[DMA ? 1 : NCH];
             int pg[NCH];
-            uint32_t there = 0;  // bit i: pass i's page is in the pool
+            uint32_t there = 0;  // 8 bits, bit i: pass i's page is in the pool
             float sreg = 0.0f;
             int spg = -1;
             const int in_page = (1 << a.kv.shift) - 1;
             const auto page_at = [&](int pos) { return pos < it.limit ? table[pos >> a.kv.shift] : -1; };
+            const auto page_of_run = [&](int pos) { return scalar(table[min(pos, it.limit - 1) >> a.kv.shift]); };
             const auto pass_row = [&](int i) { return (64 * wave + THREADS * i) / CPR; };
-            const int srow = tid % BN;  // 8-bit formats: thread's row of the k (tid < BN) or v scales
+            const int srow = tid % BN;  // 8 bits: thread's row of the k (tid < BN) or v scales
             const auto fetch_pages = [&](int kt) {
 #pragma unroll
-                for (int i = 0; i < NCH; ++i) pg[i] = page_at(kt * BN + pass_row(i));
-                if (FMT != kKvBf16 && tid < 2 * BN) spg = page_at(kt * BN + srow);
+                for (int i = 0; i < NCH; ++i) pg[i] = page_of_run(kt * BN + pass_row(i));
+                if (!DMA && tid < 2 * BN) spg = page_at(kt * BN + srow);
             };
             const auto row_of = [&](int page, int pos) {
                 return (((int64_t)page * a.kv.n_kv + head) << a.kv.shift) + (pos & in_page);
             };
-            const auto issue = [&](int kt) {
+            const auto good_of = [&](int buf) { return reinterpret_cast<int *>(lds + TL::o_ok + buf * 32); };
+            const auto issue = [&](int kt, int buf) {
                 there = 0;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     const bool in_pool = (uint32_t)pg[i] < (uint32_t)a.kv.n_pages;
-                    there |= (uint32_t)in_pool << i;
                     const int64_t at = row_of(in_pool ? pg[i] : 0, kt * BN + pass_row(i)) * (D * TL::ES);
-                    kreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.k + at + 16 * lane);
-                    vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
+                    if constexpr (DMA) {
+                        // LDS is written linearly: the swizzle is in the chunk each lane fetches
+                        const int r = pass_row(i) + lane / CPR, c = (lane % CPR) ^ (r & TL::SWZ);
+                        unsigned char *to = lds + buf * TL::buf_bytes + pass_row(i) * TL::ROWB;
+                        const int64_t from = at + (lane / CPR) * TL::ROWB + 16 * c;
+                        lds_dma16(a.kv.k + from, to + 16 * lane);
+                        lds_dma16(a.kv.v + from, to + BN * TL::ROWB + 16 * lane);
+                        if (lane % CPR == 0 && (r & 15) == 0) good_of(buf)[r >> 4] = in_pool;
+                    } else {
+                        there |= (uint32_t)in_pool << i;
+                        kreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.k + at + 16 * lane);
+                        vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
+                    }
                 }
-                if (FMT != kKvBf16 && tid < 2 * BN) {
+                if (!DMA && tid < 2 * BN) {
                     const bool in_pool = (uint32_t)spg < (uint32_t)a.kv.n_pages;
                     sreg = (tid < BN ? a.kv.ks : a.kv.vs)[row_of(in_pool ? spg : 0, kt * BN + srow)];
                     if (!in_pool) sreg = 0.0f;
                 }
             };
-            // Registers to LDS.  guard: the tile holds keys from ctx on, which some row may not see.
+            // 8 bits: registers to LDS.  tail: the tile holds keys from ctx on, which some row may not see.
             // What is not finite in their v must not meet a zero weight: it becomes 0 here, and the
             // item's end adds it for the rows that do see it.
-            const auto put = [&](int kt, bool guard) {
+            const auto put = [&](int kt, int buf, bool tail) {
+                unsigned char *kl = lds + buf * TL::buf_bytes, *vl = kl + BN * TL::ROWB;
+                if (there != (1u << NCH) - 1) {
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i)
+                        if (!((there >> i) & 1)) vreg[DMA ? 0 : i] = u32x4_t{0, 0, 0, 0};
+                }
+                if (FMT == kKvE4m3 && tail) {
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i)
+                        if (kt * BN + pass_row(i) + lane / CPR >= it.ctx && strip<FMT>(vreg[DMA ? 0 : i])) *bad = 1;
+                }
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     const int row = pass_row(i) + lane / CPR, c = lane % CPR, z = row & TL::SWZ;
-                    if (c == 0 && (row & 15) == 0) good[row >> 4] = (there >> i) & 1;
-                    bf16x8_t kk[2], vv[2];
-                    if constexpr (FMT == kKvBf16) {
-                        kk[0] = __builtin_bit_cast(bf16x8_t, kreg[i]);
-                        vv[0] = __builtin_bit_cast(bf16x8_t, vreg[i]);
-                    } else {
-                        kk[0] = widen8<FMT>(kreg[i][0], kreg[i][1]);
-                        kk[1] = widen8<FMT>(kreg[i][2], kreg[i][3]);
-                        vv[0] = widen8<FMT>(vreg[i][0], vreg[i][1]);
-                        vv[1] = widen8<FMT>(vreg[i][2], vreg[i][3]);
-                    }
+                    if (c == 0 && (row & 15) == 0) good_of(buf)[row >> 4] = (there >> i) & 1;
+                    const u32x4_t k = kreg[DMA ? 0 : i], v = vreg[DMA ? 0 : i];
 #pragma unroll
-                    for (int e = 0; e < 2 / TL::ES; ++e) {
-                        if (!((there >> i) & 1)) vv[e] = bf16x8_t{};
-                        if (FMT != kKvI8 && guard && kt * BN + row >= it.ctx) {
-                            bool any = false;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const bool off = (__builtin_bit_cast(uint16_t, (__bf16)vv[e][j]) & 0x7f80) == 0x7f80;
-                                any |= off;
-                                if (off) vv[e][j] = (__bf16)0.0f;
-                            }
-                            if (any) *bad = 1;
-                        }
-                        const int cc = FMT == kKvBf16 ? c : 2 * c + e;
-                        const int at = row * TL::ROWB + ((cc ^ z) * 16);
-                        *reinterpret_cast<bf16x8_t *>(kl + at) = kk[e];
-                        *reinterpret_cast<bf16x8_t *>(vl + at) = vv[e];
+                    for (int e = 0; e < 2; ++e) {
+                        const int at = row * TL::ROWB + (((2 * c + e) ^ z) * 16);
+                        *reinterpret_cast<u32x4_t *>(kl + at) = widen_k<FMT>(k[2 * e], k[2 * e + 1]);
+                        *reinterpret_cast<u32x4_t *>(vl + at) = widen_v<FMT>(v[2 * e], v[2 * e + 1]);
                     }
                 }
-                if (FMT != kKvBf16 && tid < 2 * BN) {
-                    if (guard && tid >= BN && kt * BN + srow >= it.ctx && !(__builtin_fabsf(sreg) < __builtin_inff())) {
-                        sreg = 0.0f;
-                        *bad = 1;
+                if (tid < 2 * BN) {
+                    float *sc = reinterpret_cast<float *>(lds + TL::o_sc + buf * TL::sc_bytes);
+                    if (tid < BN) {
+                        sc[srow] = sreg * a.scale;
+                    } else {
+                        if (tail && kt * BN + srow >= it.ctx && !(__builtin_fabsf(sreg) < __builtin_inff())) {
+                            sreg = 0.0f;
+                            *bad = 1;
+                        }
+                        const float vs = sreg == 0.0f ? 1.0f : sreg;
+                        sc[BN + srow] = __builtin_amdgcn_logf(vs);  // base 2
+                        sc[2 * BN + srow] = 1.0f / vs;
                     }
-                    (tid < BN ? ksc : vsc)[srow] = sreg;
+                }
+            };
+            // bf16: the same for a tile that lies in LDS already; between two barriers.
+            const auto strip_tile = [&](int kt, int buf) {
+                unsigned char *vl = lds + buf * TL::buf_bytes + BN * TL::ROWB;
+#pragma unroll 1
+                for (int x = tid; x < BN * CPR; x += THREADS) {
+                    const int row = x / CPR;
+                    if (kt * BN + row < it.ctx && good_of(buf)[row >> 4]) continue;
+                    u32x4_t *at = reinterpret_cast<u32x4_t *>(vl + 16 * x);
+                    u32x4_t v = *at;
+                    if (!strip<FMT>(v)) continue;
+                    *at = v;
+                    *bad = 1;
                 }
             };
             fetch_pages(kt0);
@@ -361,7 +467,9 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
                 const int rel = pos - it.ctx;
                 return ((words[rel >> 5] >> (rel & 31)) & 1) != 0;
             };
-            const auto compute = [&](int kt, bool masked) {
+            const auto compute = [&](int kt, int buf, bool masked) {
+                const unsigned char *kl = lds + buf * TL::buf_bytes, *vl = kl + BN * TL::ROWB;
+                const float *sc = reinterpret_cast<const float *>(lds + TL::o_sc + buf * TL::sc_bytes);
                 f4 s[RT][KB];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
@@ -376,27 +484,26 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
                         for (int rt = 0; rt < RT; ++rt) s[rt][kb] = mfma_kq(kf, qf[rt][ks], s[rt][kb]);
                     }
                 }
-                float top[RT];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) top[rt] = kNegInf;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
                     const int k0 = wk * KW + 16 * kb + 4 * lg;  // the lane's four keys of the block
-                    f4 c = f4{a.scale, a.scale, a.scale, a.scale};
-                    if constexpr (FMT != kKvBf16) {
-                        const f4 ks = *reinterpret_cast<const f4 *>(ksc + k0);
+                    if constexpr (DMA) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) c[i] *= ks[i];
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[rt][kb][i] *= a.scale;
+                    } else {
+                        const f4 c = *reinterpret_cast<const f4 *>(sc + k0), lv = *reinterpret_cast<const f4 *>(sc + BN + k0);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[rt][kb][i] = __builtin_fmaf(s[rt][kb][i], c[i], lv[i]);
                     }
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[rt][kb][i] *= c[i];
                 }
                 if (masked) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
-                        const bool there = good[(wk * KW >> 4) + kb] != 0;
+                        const bool here = good_of(buf)[(wk * KW >> 4) + kb] != 0;
                         const int p0 = kt * BN + wk * KW + 16 * kb + 4 * lg;
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
@@ -404,17 +511,20 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
                             for (int i = 0; i < 4; ++i) {
                                 bool on = p0 + i < seen[rt];
                                 if (!PREFIX && a.parent && !on && p0 + i < it.limit) on = in_tree(anc[rt], p0 + i);
-                                s[rt][kb][i] = on && there ? s[rt][kb][i] : kNegInf;
+                                s[rt][kb][i] = on && here ? s[rt][kb][i] : kNegInf;
                             }
                     }
                 }
+                float top[RT];
                 bool grew = false;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
+                    top[rt] = fmaxf(s[rt][0][0], s[rt][0][1]);
 #pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], s[rt][kb][i]);
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (kb > 0) top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][0]), s[rt][kb][1]);
+                        top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][2]), s[rt][kb][3]);
+                    }
                     top[rt] = quad_max(top[rt]);
                     grew |= top[rt] > m[rt];
                 }
@@ -430,20 +540,24 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
                             for (int i = 0; i < 4; ++i) o[rt][cb][i] *= f;
                     }
                 }
-                bf16x8_t pf[RT][KB / 2];
+                P8 pf[RT][KB / 2];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    f4 vs = f4{1.f, 1.f, 1.f, 1.f};
-                    if constexpr (FMT != kKvBf16) vs = *reinterpret_cast<const f4 *>(vsc + wk * KW + 16 * kb + 4 * lg);
+                    f4 iv = f4{1.f, 1.f, 1.f, 1.f};
+                    if constexpr (!DMA) iv = *reinterpret_cast<const f4 *>(sc + 2 * BN + wk * KW + 16 * kb + 4 * lg);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float mf = finite_max(m[rt]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float p = exp2_f(s[rt][kb][i] - finite_max(m[rt]));
-                            l[rt] += p;
-                            if constexpr (FMT != kKvBf16) p *= vs[i];
-                            pf[rt][kb / 2][4 * (kb % 2) + i] = (__bf16)p;
+                            const float w = exp2_f(s[rt][kb][i] - mf);
+                            if constexpr (DMA)
+                                l[rt] += w;
+                            else
+                                l[rt] = __builtin_fmaf(w, iv[i], l[rt]);
+                            pf[rt][kb / 2][4 * (kb % 2) + i] = w;
                         }
+                    }
                 }
 #pragma unroll
                 for (int kp = 0; kp < KB / 2; ++kp) {
@@ -452,31 +566,39 @@ __global__ __launch_bounds__(64 * NR * NK, OCC) void attn_kernel(AttnArgs a)
 #pragma unroll
                     for (int cb = 0; cb < D / 16; ++cb) {
                         const int c = ((2 * cb + ((li & 3) >> 1)) ^ z) * 16;
-                        const bf16x8_t vf =
-                            __builtin_bit_cast(bf16x8_t, u64x2_t{lds_tr4(base + c), lds_tr4(base + c + 16 * TL::ROWB)});
+                        const P8 vf = __builtin_bit_cast(P8, u64x2_t{lds_tr4(base + c), lds_tr4(base + c + 16 * TL::ROWB)});
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) o[rt][cb] = mfma_kq(vf, pf[rt][kp], o[rt][cb]);
+                        for (int rt = 0; rt < RT; ++rt) o[rt][cb] = mfma_vp(vf, pf[rt][kp], o[rt][cb]);
                     }
                 }
             };
 
             if (tid == 0) *bad = 0;  // before the loop's first barrier
-            issue(kt0);
+            issue(kt0, 0);
             if (kt0 + 1 < kt1) fetch_pages(kt0 + 1);
 #pragma unroll 1
             for (int kt = kt0; kt < kt1; ++kt) {
+                const int buf = NB > 1 ? (kt - kt0) & 1 : 0;
                 const bool tail = (kt + 1) * BN > it.ctx;  // keys that some row may not see
-                __syncthreads();                           // the last tile's reads are done
-                put(kt, tail);
+                // One barrier per tile with two buffers: what this tile's copy overwrites was last read two
+                // tiles ago, before the barrier between.
+                if constexpr (NB == 1) __syncthreads();
+                if constexpr (!DMA) put(kt, buf, tail);
+                if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's part of the tile is in LDS
                 __syncthreads();
                 if (kt + 1 < kt1) {
-                    issue(kt + 1);
+                    issue(kt + 1, buf ^ 1);
                     if (kt + 2 < kt1) fetch_pages(kt + 2);
                 }
                 int all = 1;
 #pragma unroll
-                for (int i = 0; i < BN / 16; ++i) all &= good[i];
-                compute(kt, tail || !__builtin_amdgcn_readfirstlane(all));
+                for (int i = 0; i < BN / 16; ++i) all &= good_of(buf)[i];
+                const bool masked = tail || !__builtin_amdgcn_readfirstlane(all);
+                if (DMA && masked) {
+                    strip_tile(kt, buf);
+                    __syncthreads();
+                }
+                compute(kt, buf, masked);
             }
 
             // ---- join the key waves: the last one ends with the item's sums
@@ -762,17 +884,57 @@ __global__ __launch_bounds__(512) void attn_join_kernel(AttnArgs a)
 
 // -------------------------------------------------------------------------------------- launches
 
-// Tile shapes by the rows that share keys: 16 or 32 rows with the keys of a 128-key tile dealt to four
-// waves, 64 rows on 2 x 2 waves, 128 rows on four waves.
+// Tile shapes by the rows that share keys (attn_config): 16, 32, 64 or 128 rows.  with_shape
+// calls f with the shape's type.
 static int attn_config(int64_t rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
-constexpr int kAttnBm[4] = {16, 32, 64, 128}, kAttnBn[4] = {128, 128, 64, 64};
+constexpr int kAttnBm[4] = {16, 32, 64, 128};
+
+template <int NR_, int NK_, int RT_, int BN_, int NB_>
+struct Shape {
+    static constexpr int NR = NR_, NK = NK_, RT = RT_, BN = BN_, NB = NB_;
+};
+template <int D, int FMT, class F>
+static auto with_shape(int cfg, F f)
+{
+    constexpr bool bf16 = FMT == kKvBf16;
+    if constexpr (D == 256) {
+        switch (cfg) {
+        case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
+        case 1: return f(Shape<2, 2, 1, 64, bf16 ? 2 : 1>{});
+        case 2: return f(Shape<2, 2, 2, 64, bf16 ? 2 : 1>{});
+        default: return f(Shape<4, 1, 2, 64, bf16 ? 2 : 1>{});
+        }
+    } else {
+        switch (cfg) {
+        case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
+        case 1: return f(Shape<1, 2, 2, 64, bf16 ? 2 : 1>{});
+        case 2: return f(Shape<2, 2, 2, 64, 2>{});
+        default: return f(Shape<4, 1, 2, 64, 2>{});
+        }
+    }
+}
+template <int D, int FMT>
+static void tile_sizes(int cfg, int &bn, int &per_cu)
+{
+    with_shape<D, FMT>(cfg, [&](auto s) {
+        using S = decltype(s);
+        bn = S::BN;
+        per_cu = AttnTile<D, FMT, S::NR, S::NK, S::RT, S::BN, S::NB>::per_cu;
+    });
+}
+template <int D>
+static void tile_sizes_f(int format, int cfg, int &bn, int &per_cu)
+{
+    format == kKvBf16   ? tile_sizes<D, kKvBf16>(cfg, bn, per_cu)
+    : format == kKvE4m3 ? tile_sizes<D, kKvE4m3>(cfg, bn, per_cu)
+                        : tile_sizes<D, kKvI8>(cfg, bn, per_cu);
+}
 
 bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch, int n_tok, int max_pages, bool prefix,
                int max_prefix_pages, AttnPlan &p)
 {
-    (void)format;
     p = AttnPlan{};
-    const int cus = 256, per_cu = d == 256 ? 1 : 2;
+    constexpr int kCus = 256;
     size_t at = 0;
     const auto room = [&](size_t bytes) {
         const size_t o = at;
@@ -783,7 +945,10 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
     const auto phase = [&](AttnPhase &ph, int64_t rows, int entries, int64_t pages) {
         ph.cfg = attn_config(rows);
         ph.bm = kAttnBm[ph.cfg];
-        ph.bn = kAttnBn[ph.cfg];
+        int per_cu = 1;
+        d == 64 ? tile_sizes_f<64>(format, ph.cfg, ph.bn, per_cu)
+        : d == 128 ? tile_sizes_f<128>(format, ph.cfg, ph.bn, per_cu)
+                   : tile_sizes_f<256>(format, ph.cfg, ph.bn, per_cu);
         const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
         const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
         if (items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
@@ -793,8 +958,8 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
         }
         ph.row_tiles = (int)row_tiles;
         ph.items = (int)items;
-        ph.wgs = (int)std::min<int64_t>(cus * per_cu, items * n_kv * tiles);
-        const size_t slots = (size_t)(items * n_kv) + cus * per_cu;
+        ph.wgs = (int)std::min<int64_t>(kCus * per_cu, items * n_kv * tiles);
+        const size_t slots = (size_t)(items * n_kv) + kCus * per_cu;
         ph.per = room(4);
         ph.first = room((size_t)(items * n_kv) * 4);
         ph.pml = room(slots * ph.bm * 8);
@@ -812,25 +977,17 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
     return fits;
 }
 
-template <int D, int FMT, int NR, int NK, int RT, int BN, int OCC, bool PREFIX>
-static hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream)
-{
-    using TL = AttnTile<D, FMT, NR, NK, RT, BN, OCC>;
-    const AttnPhase &ph = PREFIX ? a.plan.prefix : a.plan.suffix;
-    hipLaunchKernelGGL((attn_kernel<D, FMT, NR, NK, RT, BN, OCC, PREFIX>), dim3(ph.wgs), dim3(TL::THREADS), TL::lds, stream, a);
-    return hipGetLastError();
-}
-
 template <int D, int FMT, bool PREFIX>
 static hipError_t launch_cfg(const AttnArgs &a, hipStream_t stream)
 {
-    constexpr int OCC = D == 256 ? 1 : 2;  // waves per SIMD that the registers must allow
-    switch ((PREFIX ? a.plan.prefix : a.plan.suffix).cfg) {
-    case 0: return launch_tiles<D, FMT, 1, 4, 1, 128, OCC, PREFIX>(a, stream);
-    case 1: return launch_tiles<D, FMT, 1, 4, 2, 128, OCC, PREFIX>(a, stream);
-    case 2: return launch_tiles<D, FMT, 2, 2, 2, 64, OCC, PREFIX>(a, stream);
-    default: return launch_tiles<D, FMT, 4, 1, 2, 64, OCC, PREFIX>(a, stream);
-    }
+    const AttnPhase &ph = PREFIX ? a.plan.prefix : a.plan.suffix;
+    return with_shape<D, FMT>(ph.cfg, [&](auto s) {
+        using S = decltype(s);
+        using TL = AttnTile<D, FMT, S::NR, S::NK, S::RT, S::BN, S::NB>;
+        hipLaunchKernelGGL((attn_kernel<D, FMT, S::NR, S::NK, S::RT, S::BN, S::NB, PREFIX>), dim3(ph.wgs), dim3(TL::THREADS),
+                           TL::lds, stream, a);
+        return hipGetLastError();
+    });
 }
 
 template <int D>
