@@ -181,28 +181,30 @@ struct Item {
     int tiles;
 };
 
-template <bool PREFIX>
+// BM_, BN_: the tile's rows and keys where they are known, 0 to take them from the phase.
+template <bool PREFIX, int BM_ = 0, int BN_ = 0>
 __device__ __forceinline__ Item attn_item(const AttnArgs &a, const AttnPhase &ph, int item)
 {
+    const int bm = BM_ ? BM_ : ph.bm, bn = BN_ ? BN_ : ph.bn;
     Item it{};
     if constexpr (PREFIX) {
         const int *live = reinterpret_cast<const int *>(a.ws + a.plan.live);
-        it.row0 = item * ph.bm;
+        it.row0 = item * bm;
         it.rows = (a.b.n_new ? live[0] : a.b.n_batch * a.b.n_tok) * a.grp;
         const int64_t cap = (int64_t)a.max_prefix_pages << a.kv.shift;
         it.limit = it.ctx = (int)min((int64_t)max(a.prefix_len[0], 0), cap);
-        it.tiles = it.row0 < it.rows ? (it.limit + ph.bn - 1) / ph.bn : 0;
+        it.tiles = it.row0 < it.rows ? (it.limit + bn - 1) / bn : 0;
     } else {
-        it.entry = item / ph.row_tiles;
-        it.row0 = (item - it.entry * ph.row_tiles) * ph.bm;
+        it.entry = ph.row_tiles == 1 ? item : item / ph.row_tiles;
+        it.row0 = (item - it.entry * ph.row_tiles) * bm;
         const int start = a.b.start[it.entry], n = kv_new(a.b, it.entry);
         it.rows = n * a.grp;
         // a chain's last row of the tile sees no key after its own token
-        const int last = a.parent ? n - 1 : (max(min(it.row0 + ph.bm, it.rows), 1) - 1) / a.grp;
+        const int last = a.parent ? n - 1 : (max(min(it.row0 + bm, it.rows), 1) - 1) / a.grp;
         const int64_t cap = (int64_t)a.b.max_pages << a.kv.shift;
         it.ctx = (int)min((int64_t)max(start, 0), cap);
         it.limit = (int)min((int64_t)max(start, 0) + last + 1, cap);
-        it.tiles = start >= 0 && it.row0 < it.rows ? (it.limit + ph.bn - 1) / ph.bn : 0;
+        it.tiles = start >= 0 && it.row0 < it.rows ? (it.limit + bn - 1) / bn : 0;
     }
     return it;
 }
@@ -230,7 +232,7 @@ struct AttnTile {
                          o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
     static constexpr int waves = NR * NK;
     // workgroups per CU: by LDS, and eight waves (two per SIMD) where the registers allow that
-    static constexpr int by_lds = 160 * 1024 / lds, occ = D == 256 && RT == 2 && waves == 4 ? 1 : 2;
+    static constexpr int by_lds = 160 * 1024 / lds, occ = D == 256 ? (!DMA && waves == 2 ? 1 : 2) : waves == 2 || RT == 2 ? 2 : waves == 4 && D == 128 ? 3 : 4;
     static constexpr int by_waves = 4 * occ / waves, per_cu = by_lds < by_waves ? by_lds : by_waves;
     static_assert(KW % 32 == 0 && NCH >= 1 && BN * CPR % THREADS == 0 && BN <= 128, "tile");
     static_assert(DMA ? NB == 2 : 2 * BN <= THREADS, "staging");
@@ -260,10 +262,11 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
     // the kernel is held in scalar registers: values kept in vector registers across lane-dependent
     // branches have come back wrong from spills that the compiler restored with no lane active.
     const int chunk = (ph.items + THREADS - 1) / THREADS;
-    int mine = 0;
+    int mine = 0, t_last = 0;
     for (int j = 0; j < chunk; ++j) {
-        const int i = tid * chunk + j, t = attn_item<PREFIX>(a, ph, min(i, ph.items - 1)).tiles;
-        mine += i < ph.items ? t : 0;
+        const int i = tid * chunk + j;
+        t_last = attn_item<PREFIX, BM, BN>(a, ph, min(i, ph.items - 1)).tiles;
+        mine += i < ph.items ? t_last : 0;
     }
     int upto = mine;  // inclusive scan: waves, then across them
 #pragma unroll
@@ -290,7 +293,8 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
     {
         const int rem = (int)(unit - (uint32_t)head * (uint32_t)total_head);
         for (int j = 0; j < chunk; ++j) {
-            const int i = tid * chunk + j, t = attn_item<PREFIX>(a, ph, min(i, ph.items - 1)).tiles;
+            const int i = tid * chunk + j;
+            const int t = chunk == 1 ? t_last : attn_item<PREFIX, BM, BN>(a, ph, min(i, ph.items - 1)).tiles;
             if (i < ph.items && rem >= before && rem < before + t) {  // one lane of the workgroup, once
                 scan[THREADS] = i;
                 scan[THREADS + 1] = rem - before;
@@ -302,7 +306,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
     int item = scalar(scan[THREADS]), off = scalar(scan[THREADS + 1]);
 
     while (unit < end) {
-        Item it = attn_item<PREFIX>(a, ph, item);
+        Item it = attn_item<PREFIX, BM, BN>(a, ph, item);
         it.entry = scalar(it.entry);
         it.row0 = scalar(it.row0);
         it.rows = scalar(it.rows);
@@ -315,36 +319,40 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 reinterpret_cast<uint32_t *>(a.ws + ph.first)[head * ph.items + item] = unit;
             const int *table = PREFIX ? a.prefix_pages : a.b.table + (int64_t)it.entry * a.b.max_pages;
 
-            // ---- staging.  The pages a tile lies on are read two tiles ahead, its rows one tile ahead
+            // ---- staging.  A tile's rows are read one tile ahead
             // (bf16: into the other LDS buffer; 8 bits: into registers).  A wave's rows of one pass lie
             // in one aligned run of at most 16, so on one page: its address is uniform but for the
             // lane's fixed offset.  Every load is made: a page that is not in the pool becomes page 0, rows
             // past the limit come from the page that holds its last one, and no query row sees either.
             u32x4_t kreg[DMA ? 1 : NCH], vreg[DMA ? 1 : NCH];
-            int pg[NCH];
             uint32_t there = 0;  // 8 bits, bit i: pass i's page is in the pool
             float sreg = 0.0f;
-            int spg = -1;
             const int in_page = (1 << a.kv.shift) - 1;
-            const auto page_at = [&](int pos) { return pos < it.limit ? table[pos >> a.kv.shift] : -1; };
-            const auto page_of_run = [&](int pos) { return scalar(table[min(pos, it.limit - 1) >> a.kv.shift]); };
+            // Table entries p0 .. p0 + 63 of the item's run of pages, one per lane: a page is then a lane
+            // read away (a load per tile would be waited for, 1.2k - 3.8k clocks of a tile's ~6k).
+            const int last_page = (it.limit - 1) >> a.kv.shift;
+            int p0 = (kt0 * BN) >> a.kv.shift, pages = table[min(p0 + lane, last_page)];
+            const auto page_of_run = [&](int pos) {
+                return __builtin_amdgcn_readlane(pages, (min(pos, it.limit - 1) >> a.kv.shift) - p0);
+            };
             const auto pass_row = [&](int i) { return (64 * wave + THREADS * i) / CPR; };
             const int srow = tid % BN;  // 8 bits: thread's row of the k (tid < BN) or v scales
-            const auto fetch_pages = [&](int kt) {
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) pg[i] = page_of_run(kt * BN + pass_row(i));
-                if (!DMA && tid < 2 * BN) spg = page_at(kt * BN + srow);
-            };
             const auto row_of = [&](int page, int pos) {
                 return (((int64_t)page * a.kv.n_kv + head) << a.kv.shift) + (pos & in_page);
             };
             const auto good_of = [&](int buf) { return reinterpret_cast<int *>(lds + TL::o_ok + buf * 32); };
             const auto issue = [&](int kt, int buf) {
+                const int end_page = min(kt * BN + BN - 1, it.limit - 1) >> a.kv.shift;
+                if (end_page >= p0 + 64) {
+                    p0 = (kt * BN) >> a.kv.shift;
+                    pages = table[min(p0 + lane, last_page)];
+                }
                 there = 0;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    const bool in_pool = (uint32_t)pg[i] < (uint32_t)a.kv.n_pages;
-                    const int64_t at = row_of(in_pool ? pg[i] : 0, kt * BN + pass_row(i)) * (D * TL::ES);
+                    const int pg = page_of_run(kt * BN + pass_row(i));
+                    const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
+                    const int64_t at = row_of(in_pool ? pg : 0, kt * BN + pass_row(i)) * (D * TL::ES);
                     if constexpr (DMA) {
                         // LDS is written linearly: the swizzle is in the chunk each lane fetches
                         const int r = pass_row(i) + lane / CPR, c = (lane % CPR) ^ (r & TL::SWZ);
@@ -359,10 +367,14 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
                     }
                 }
-                if (!DMA && tid < 2 * BN) {
-                    const bool in_pool = (uint32_t)spg < (uint32_t)a.kv.n_pages;
-                    sreg = (tid < BN ? a.kv.ks : a.kv.vs)[row_of(in_pool ? spg : 0, kt * BN + srow)];
-                    if (!in_pool) sreg = 0.0f;
+                if constexpr (!DMA) {
+                    // all lanes: the pages are in lanes
+                    const int pg = __shfl(pages, (min(kt * BN + srow, it.limit - 1) >> a.kv.shift) - p0);
+                    const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
+                    if (tid < 2 * BN) {
+                        sreg = (tid < BN ? a.kv.ks : a.kv.vs)[row_of(in_pool ? pg : 0, kt * BN + srow)];
+                        sreg = in_pool ? sreg : 0.0f;
+                    }
                 }
             };
             // 8 bits: registers to LDS.  tail: the tile holds keys from ctx on, which some row may not see.
@@ -421,7 +433,6 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                     *bad = 1;
                 }
             };
-            fetch_pages(kt0);
 
             // ---- the tile's query rows: B operand, lane li holds row li of each 16-row block
             bf16x8_t qf[RT][D / 32];
@@ -484,6 +495,15 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         for (int rt = 0; rt < RT; ++rt) s[rt][kb] = mfma_kq(kf, qf[rt][ks], s[rt][kb]);
                     }
                 }
+                float top[RT];
+                const auto maxima = [&](int kb) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        if (kb == 0) top[rt] = fmaxf(s[rt][0][0], s[rt][0][1]);
+                        if (kb > 0) top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][0]), s[rt][kb][1]);
+                        top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][2]), s[rt][kb][3]);
+                    }
+                };
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
                     const int k0 = wk * KW + 16 * kb + 4 * lg;  // the lane's four keys of the block
@@ -499,6 +519,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 #pragma unroll
                             for (int i = 0; i < 4; ++i) s[rt][kb][i] = __builtin_fmaf(s[rt][kb][i], c[i], lv[i]);
                     }
+                    maxima(kb);
                 }
                 if (masked) {
 #pragma unroll
@@ -513,18 +534,12 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                                 if (!PREFIX && a.parent && !on && p0 + i < it.limit) on = in_tree(anc[rt], p0 + i);
                                 s[rt][kb][i] = on && here ? s[rt][kb][i] : kNegInf;
                             }
+                        maxima(kb);
                     }
                 }
-                float top[RT];
                 bool grew = false;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    top[rt] = fmaxf(s[rt][0][0], s[rt][0][1]);
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        if (kb > 0) top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][0]), s[rt][kb][1]);
-                        top[rt] = fmaxf(fmaxf(top[rt], s[rt][kb][2]), s[rt][kb][3]);
-                    }
                     top[rt] = quad_max(top[rt]);
                     grew |= top[rt] > m[rt];
                 }
@@ -575,7 +590,6 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 
             if (tid == 0) *bad = 0;  // before the loop's first barrier
             issue(kt0, 0);
-            if (kt0 + 1 < kt1) fetch_pages(kt0 + 1);
 #pragma unroll 1
             for (int kt = kt0; kt < kt1; ++kt) {
                 const int buf = NB > 1 ? (kt - kt0) & 1 : 0;
@@ -586,10 +600,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 if constexpr (!DMA) put(kt, buf, tail);
                 if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's part of the tile is in LDS
                 __syncthreads();
-                if (kt + 1 < kt1) {
-                    issue(kt + 1, buf ^ 1);
-                    if (kt + 2 < kt1) fetch_pages(kt + 2);
-                }
+                if (kt + 1 < kt1) issue(kt + 1, buf ^ 1);
                 int all = 1;
 #pragma unroll
                 for (int i = 0; i < BN / 16; ++i) all &= good_of(buf)[i];
@@ -653,7 +664,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 if (__builtin_amdgcn_readfirstlane(*bad)) {
 #pragma unroll 1
                     for (int pos = max(it.ctx, kt0 * BN); pos < min(it.limit, kt1 * BN); ++pos) {
-                        const int page = page_at(pos);
+                        const int page = scalar(table[pos >> a.kv.shift]);
                         if ((uint32_t)page >= (uint32_t)a.kv.n_pages) continue;
                         const int64_t at = row_of(page, pos);
                         const bool none = FMT != kKvBf16 && !(__builtin_fabsf(a.kv.vs[at]) < __builtin_inff());
@@ -897,20 +908,11 @@ template <int D, int FMT, class F>
 static auto with_shape(int cfg, F f)
 {
     constexpr bool bf16 = FMT == kKvBf16;
-    if constexpr (D == 256) {
-        switch (cfg) {
-        case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
-        case 1: return f(Shape<2, 2, 1, 64, bf16 ? 2 : 1>{});
-        case 2: return f(Shape<2, 2, 2, 64, bf16 ? 2 : 1>{});
-        default: return f(Shape<4, 1, 2, 64, bf16 ? 2 : 1>{});
-        }
-    } else {
-        switch (cfg) {
-        case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
-        case 1: return f(Shape<1, 2, 2, 64, bf16 ? 2 : 1>{});
-        case 2: return f(Shape<2, 2, 2, 64, 2>{});
-        default: return f(Shape<4, 1, 2, 64, 2>{});
-        }
+    switch (cfg) {
+    case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
+    case 1: return f(Shape<2, 2, 1, 64, bf16 ? 2 : 1>{});
+    case 2: return f(Shape<4, 1, 1, 64, bf16 ? 2 : 1>{});
+    default: return f(Shape<D == 64 ? 4 : 8, 1, D == 64 ? 2 : 1, 64, 2>{});
     }
 }
 template <int D, int FMT>
