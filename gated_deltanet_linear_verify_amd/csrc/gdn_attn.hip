@@ -227,8 +227,8 @@ struct AttnTile {
     static constexpr int buf_bytes = 2 * BN * ROWB, merge_bytes = NK > 1 ? BM * D * 4 : 0;
     static constexpr int tile_bytes = NB * buf_bytes > merge_bytes ? NB * buf_bytes : merge_bytes;
     static constexpr int sc_bytes = DMA ? 0 : 3 * BN * 4;        // k scale | log2 v scale | 1 / v scale
-    // K and V buffers (reused to join the waves' outputs) | scales | good blocks | bad | scan | m, l
-    static constexpr int o_sc = tile_bytes, o_ok = o_sc + NB * sc_bytes, o_bad = o_ok + NB * 32, o_scan = o_bad + 16,
+    // K and V buffers (reused to join the waves' outputs) | scales | bad | scan | m, l
+    static constexpr int o_sc = tile_bytes, o_bad = o_sc + NB * sc_bytes, o_scan = o_bad + 16,
                          o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
     static constexpr int waves = NR * NK;
     // workgroups per CU: by LDS, and eight waves (two per SIMD) where the registers allow that
@@ -325,13 +325,14 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
             // lane's fixed offset.  Every load is made: a page that is not in the pool becomes page 0, rows
             // past the limit come from the page that holds its last one, and no query row sees either.
             u32x4_t kreg[DMA ? 1 : NCH], vreg[DMA ? 1 : NCH];
-            uint32_t there = 0;  // 8 bits, bit i: pass i's page is in the pool
+            uint32_t gone = 0, gone_next = 0;  // bit i: rows 16 i .. of the tile (of the next one) have no page in the pool
             float sreg = 0.0f;
             const int in_page = (1 << a.kv.shift) - 1;
             // Table entries p0 .. p0 + 63 of the item's run of pages, one per lane: a page is then a lane
             // read away (a load per tile would be waited for, 1.2k - 3.8k clocks of a tile's ~6k).
             const int last_page = (it.limit - 1) >> a.kv.shift;
             int p0 = (kt0 * BN) >> a.kv.shift, pages = table[min(p0 + lane, last_page)];
+            uint64_t absent = __ballot((uint32_t)pages >= (uint32_t)a.kv.n_pages);  // lanes whose page is not in the pool
             const auto page_of_run = [&](int pos) {
                 return __builtin_amdgcn_readlane(pages, (min(pos, it.limit - 1) >> a.kv.shift) - p0);
             };
@@ -340,14 +341,17 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
             const auto row_of = [&](int page, int pos) {
                 return (((int64_t)page * a.kv.n_kv + head) << a.kv.shift) + (pos & in_page);
             };
-            const auto good_of = [&](int buf) { return reinterpret_cast<int *>(lds + TL::o_ok + buf * 32); };
             const auto issue = [&](int kt, int buf) {
                 const int end_page = min(kt * BN + BN - 1, it.limit - 1) >> a.kv.shift;
                 if (end_page >= p0 + 64) {
                     p0 = (kt * BN) >> a.kv.shift;
                     pages = table[min(p0 + lane, last_page)];
+                    absent = __ballot((uint32_t)pages >= (uint32_t)a.kv.n_pages);
                 }
-                there = 0;
+                gone_next = 0;
+#pragma unroll
+                for (int i = 0; i < BN / 16; ++i)
+                    gone_next |= (uint32_t)((absent >> ((min(kt * BN + 16 * i, it.limit - 1) >> a.kv.shift) - p0)) & 1) << i;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     const int pg = page_of_run(kt * BN + pass_row(i));
@@ -360,9 +364,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         const int64_t from = at + (lane / CPR) * TL::ROWB + 16 * c;
                         lds_dma16(a.kv.k + from, to + 16 * lane);
                         lds_dma16(a.kv.v + from, to + BN * TL::ROWB + 16 * lane);
-                        if (lane % CPR == 0 && (r & 15) == 0) good_of(buf)[r >> 4] = in_pool;
                     } else {
-                        there |= (uint32_t)in_pool << i;
                         kreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.k + at + 16 * lane);
                         vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
                     }
@@ -382,10 +384,10 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
             // item's end adds it for the rows that do see it.
             const auto put = [&](int kt, int buf, bool tail) {
                 unsigned char *kl = lds + buf * TL::buf_bytes, *vl = kl + BN * TL::ROWB;
-                if (there != (1u << NCH) - 1) {
+                if (gone) {
 #pragma unroll
                     for (int i = 0; i < NCH; ++i)
-                        if (!((there >> i) & 1)) vreg[DMA ? 0 : i] = u32x4_t{0, 0, 0, 0};
+                        if ((gone >> (pass_row(i) >> 4)) & 1) vreg[DMA ? 0 : i] = u32x4_t{0, 0, 0, 0};
                 }
                 if (FMT == kKvE4m3 && tail) {
 #pragma unroll
@@ -395,7 +397,6 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
                     const int row = pass_row(i) + lane / CPR, c = lane % CPR, z = row & TL::SWZ;
-                    if (c == 0 && (row & 15) == 0) good_of(buf)[row >> 4] = (there >> i) & 1;
                     const u32x4_t k = kreg[DMA ? 0 : i], v = vreg[DMA ? 0 : i];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -425,7 +426,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 #pragma unroll 1
                 for (int x = tid; x < BN * CPR; x += THREADS) {
                     const int row = x / CPR;
-                    if (kt * BN + row < it.ctx && good_of(buf)[row >> 4]) continue;
+                    if (kt * BN + row < it.ctx && !((gone >> (row >> 4)) & 1)) continue;
                     u32x4_t *at = reinterpret_cast<u32x4_t *>(vl + 16 * x);
                     u32x4_t v = *at;
                     if (!strip<FMT>(v)) continue;
@@ -524,7 +525,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 if (masked) {
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb) {
-                        const bool here = good_of(buf)[(wk * KW >> 4) + kb] != 0;
+                        const bool here = !((gone >> ((wk * KW >> 4) + kb)) & 1);
                         const int p0 = kt * BN + wk * KW + 16 * kb + 4 * lg;
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
@@ -596,15 +597,13 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 const bool tail = (kt + 1) * BN > it.ctx;  // keys that some row may not see
                 // One barrier per tile with two buffers: what this tile's copy overwrites was last read two
                 // tiles ago, before the barrier between.
+                gone = gone_next;
                 if constexpr (NB == 1) __syncthreads();
                 if constexpr (!DMA) put(kt, buf, tail);
                 if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's part of the tile is in LDS
                 __syncthreads();
                 if (kt + 1 < kt1) issue(kt + 1, buf ^ 1);
-                int all = 1;
-#pragma unroll
-                for (int i = 0; i < BN / 16; ++i) all &= good_of(buf)[i];
-                const bool masked = tail || !__builtin_amdgcn_readfirstlane(all);
+                const bool masked = tail || gone != 0;
                 if (DMA && masked) {
                     strip_tile(kt, buf);
                     __syncthreads();
@@ -730,25 +729,25 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 
 // ---------------------------------------------------------------------------- before and after
 
-// Bit j of node t's words: node t sees drafted node j, its ancestor or itself.
+// Bit j of node t's words: node t sees drafted node j, its ancestor or itself.  A block per entry, whose
+// parents lie in LDS: a walk up is a chain of dependent reads.
 __global__ __launch_bounds__(256) void attn_ancestors_kernel(AttnArgs a)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)a.b.n_batch * a.b.n_tok) return;
-    const int64_t b = i / a.b.n_tok;
-    const int32_t *parent = a.parent + b * a.b.n_tok;
-    uint32_t *w = reinterpret_cast<uint32_t *>(a.ws + a.plan.anc) + i * a.plan.words;
-    int node = (int)(i - b * a.b.n_tok), up = 0;
-    for (int word = a.plan.words - 1; word >= 0; --word) {
-        uint32_t bits = 0;
-        while (node >= 32 * word) {  // a parent comes before its child, so the walk ends
-            bits |= 1u << (node & 31);
-            up = parent[node];
-            node = up < node ? up : -1;
-            if (node < 0) node = -1;
-            if (node < 0) break;
+    __shared__ int up[1024];
+    const int64_t first = (int64_t)blockIdx.x * a.b.n_tok;
+    for (int t = threadIdx.x; t < a.b.n_tok; t += 256) {
+        const int p = a.parent[first + t];
+        up[t] = p >= 0 && p < t ? p : -1;
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < a.b.n_tok; t += 256) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(a.ws + a.plan.anc) + (first + t) * a.plan.words;
+        int node = t;
+        for (int word = a.plan.words - 1; word >= 0; --word) {
+            uint32_t bits = 0;
+            for (; node >= 32 * word; node = up[node]) bits |= 1u << (node & 31);  // a parent comes before its child
+            w[word] = bits;
         }
-        w[word] = bits;
     }
 }
 
@@ -785,112 +784,98 @@ struct Parts {
     int64_t slot;
     int n, row;
 };
-template <bool PREFIX>
-__device__ __forceinline__ Parts attn_parts(const AttnArgs &a, const AttnPhase &ph, int item, int row, int head)
+__device__ __forceinline__ Parts attn_parts(const AttnPhase &ph, const Item &it, uint32_t per, uint32_t first, int item, int row,
+                                            int head)
 {
-    const Item it = attn_item<PREFIX>(a, ph, item);
-    if (it.tiles <= 0) return Parts{0, 0, 0};
-    const uint32_t per = *reinterpret_cast<const uint32_t *>(a.ws + ph.per);
-    const uint32_t u = reinterpret_cast<const uint32_t *>(a.ws + ph.first)[head * ph.items + item];
-    const uint32_t w0 = u / per, w1 = (u + it.tiles - 1) / per;
-    return Parts{(int64_t)head * ph.items + item + w0, (int)(w1 - w0 + 1), row - it.row0};
+    const uint32_t w0 = first / per, w1 = (first + it.tiles - 1) / per;
+    return Parts{(int64_t)head * ph.items + item + w0, it.tiles > 0 ? (int)(w1 - w0 + 1) : 0, row - it.row0};
 }
 
-// One row of the result from its parts: WPR waves share a row (many parts: few rows with long
-// contexts), the block's other waves take other rows.
-template <int D, int WPR>
-__global__ __launch_bounds__(512) void attn_join_kernel(AttnArgs a)
+// Rows of the result from their parts.  D / 4 threads take a row, four channels each; with SPLIT the
+// block's groups of that many threads share one row (few rows can have many parts: long contexts),
+// otherwise each has its own.  What a row has to look up (its lengths, its place in the prefix's rows,
+// its items' first units) is read before any of it is used: one wait instead of a chain of them.
+template <int D, bool SPLIT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
-    constexpr int E = D / 64, ROWS = 8 / WPR;
-    __shared__ float so[8][D];
-    __shared__ float2 sml[8];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % WPR;
-    const int n_q = a.kv.n_kv * a.grp;
-    const int64_t id = (int64_t)blockIdx.x * ROWS + wave / WPR;
-    const int64_t tokrow = id / n_q;
-    const int hq = (int)(id - tokrow * n_q), head = hq / a.grp, g = hq - head * a.grp;
-    const int b = (int)(tokrow / a.b.n_tok), t = (int)(tokrow - (int64_t)b * a.b.n_tok);
-    bool work = tokrow < (int64_t)a.b.n_batch * a.b.n_tok && a.b.start[min(b, a.b.n_batch - 1)] >= 0 &&
-                t < kv_new(a.b, min(b, a.b.n_batch - 1));
-    Parts own{0, 0, 0}, pre{0, 0, 0};
-    if (work) {
-        const AttnPhase &sp = a.plan.suffix, &pp = a.plan.prefix;
-        int r = t * a.grp + g;
-        own = attn_parts<false>(a, sp, b * sp.row_tiles + r / sp.bm, r, head);
-        if (a.prefix_pages) {
-            const int at = a.b.n_new ? reinterpret_cast<const int *>(a.ws + a.plan.rank)[tokrow] : (int)tokrow;
-            r = at * a.grp + g;
-            pre = attn_parts<true>(a, pp, r / pp.bm, r, head);
-        } else if (own.n == 1) {
-            work = false;  // written whole
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+    __shared__ f4 so[SPLIT ? GROUPS : 1][LANES];
+    __shared__ float2 sml[SPLIT ? GROUPS : 1];
+    const int c = threadIdx.x % LANES, group = threadIdx.x / LANES, sub = SPLIT ? group : 0;
+    const int id = SPLIT ? (int)blockIdx.x : (int)blockIdx.x * GROUPS + group;  // row of the head: token row, query head of the group
+    const int head = blockIdx.y, rr = min(id, rows - 1);
+    const int tokrow = rr / a.grp, g = rr - tokrow * a.grp, b = tokrow / a.b.n_tok, t = tokrow - b * a.b.n_tok;
+    const AttnPhase &sp = a.plan.suffix, &pp = a.plan.prefix;
+    const int r = t * a.grp + g, item = b * sp.row_tiles + r / sp.bm;
+    const uint32_t sfirst = reinterpret_cast<const uint32_t *>(a.ws + sp.first)[head * sp.items + item];
+    const uint32_t sper = *reinterpret_cast<const uint32_t *>(a.ws + sp.per);
+    const Item it = attn_item<false>(a, sp, item);
+    const bool live = id < rows && a.b.start[b] >= 0 && t < kv_new(a.b, b);
+    Parts own = attn_parts(sp, it, max(sper, 1u), sfirst, item, r, head), pre{0, 0, 0};
+    if (a.prefix_pages) {
+        const int at = a.b.n_new ? reinterpret_cast<const int *>(a.ws + a.plan.rank)[tokrow] : tokrow;
+        const int pr = (live ? at : 0) * a.grp + g, pitem = pr / pp.bm;
+        const uint32_t pfirst = reinterpret_cast<const uint32_t *>(a.ws + pp.first)[head * pp.items + pitem];
+        const uint32_t pper = *reinterpret_cast<const uint32_t *>(a.ws + pp.per);
+        pre = attn_parts(pp, attn_item<true>(a, pp, pitem), max(pper, 1u), pfirst, pitem, pr, head);
+    }
+    const bool work = live && (a.prefix_pages || own.n > 1);  // else written whole, or not at all
+    const int n_pre = work ? pre.n : 0, n = work ? n_pre + own.n : 0;
+    const float *spo = reinterpret_cast<const float *>(a.ws + sp.po), *ppo = reinterpret_cast<const float *>(a.ws + pp.po);
+    const float2 *spml = reinterpret_cast<const float2 *>(a.ws + sp.pml), *ppml = reinterpret_cast<const float2 *>(a.ws + pp.pml);
+    float m = kNegInf, l = 0.0f;
+    f4 o = f4{0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 4;  // parts in flight
+    for (int j0 = sub; j0 < n; j0 += (SPLIT ? GROUPS : 1) * U) {
+        f4 x[U];
+        float2 y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + (SPLIT ? GROUPS : 1) * u;
+            x[u] = f4{0.f, 0.f, 0.f, 0.f};
+            y[u] = make_float2(kNegInf, 0.0f);
+            if (j >= n) continue;
+            const bool p = j < n_pre;
+            const int64_t at = p ? (pre.slot + j) * pp.bm + pre.row : (own.slot + j - n_pre) * sp.bm + own.row;
+            y[u] = (p ? ppml : spml)[at];
+            x[u] = *reinterpret_cast<const f4 *>((p ? ppo : spo) + at * D + 4 * c);
         }
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) mn = fmaxf(mn, y[u].x);
+        const float f = exp2_f(m - finite_max(mn));
+        l *= f;
+        o *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = exp2_f(y[u].x - finite_max(mn));
+            l += w * y[u].y;
+            o += w * x[u];
+        }
+        m = mn;
     }
-    float m = kNegInf, l = 0.0f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    if (work) {
-        const auto take = [&](const AttnPhase &ph, const Parts &p) {
-            const float *po = reinterpret_cast<const float *>(a.ws + ph.po);
-            const float2 *pml = reinterpret_cast<const float2 *>(a.ws + ph.pml);
-            constexpr int U = 8;  // parts in flight
-            for (int j0 = sub; j0 < p.n; j0 += WPR * U) {
-                float x[U][E];
-                float2 y[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    y[u] = make_float2(kNegInf, 0.0f);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
-                    const int j = j0 + WPR * u;
-                    if (j >= p.n) continue;
-                    const int64_t at = (p.slot + j) * ph.bm + p.row;
-                    y[u] = pml[at];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = po[at * D + E * lane + e];
-                }
-                float mn = m;
-#pragma unroll
-                for (int u = 0; u < U; ++u) mn = fmaxf(mn, y[u].x);
-                const float f = exp2_f(m - finite_max(mn));
-                l *= f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float w = exp2_f(y[u].x - finite_max(mn));
-                    l += w * y[u].y;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] += w * x[u][e];
-                }
-                m = mn;
-            }
-        };
-        if (a.prefix_pages) take(a.plan.prefix, pre);
-        take(a.plan.suffix, own);
-    }
-    if constexpr (WPR > 1) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) so[wave][E * lane + e] = o[e];
-        if (lane == 0) sml[wave] = make_float2(m, l);
+    if constexpr (SPLIT) {
+        so[group][c] = o;
+        if (c == 0) sml[group] = make_float2(m, l);
         __syncthreads();
-        if (sub != 0) return;
         float mn = kNegInf;
-        for (int w = 0; w < WPR; ++w) mn = fmaxf(mn, sml[wave + w].x);
+        for (int w = 0; w < GROUPS; ++w) mn = fmaxf(mn, sml[w].x);
         l = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.0f;
-        for (int w = 0; w < WPR; ++w) {
-            const float f = exp2_f(sml[wave + w].x - finite_max(mn));
-            l += f * sml[wave + w].y;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += f * so[wave + w][E * lane + e];
+        o = f4{0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < GROUPS; ++w) {
+            const float f = exp2_f(sml[w].x - finite_max(mn));
+            l += f * sml[w].y;
+            o += f * so[w][c];
         }
     }
-    if (!work) return;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __bf16 *out = static_cast<__bf16 *>(a.out.p) + tokrow * a.out.ld + (int64_t)hq * a.out.hd + E * lane;
+    if (work && sub == 0) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        bf16x4_t y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = (__bf16)(o[e] * inv);
+        for (int e = 0; e < 4; ++e) y[e] = (__bf16)(o[e] * inv);
+        __bf16 *out = static_cast<__bf16 *>(a.out.p) + tokrow * a.out.ld + (int64_t)(head * a.grp + g) * a.out.hd + 4 * c;
+        *reinterpret_cast<bf16x4_t *>(out) = y;
+    }
 }
 
 // -------------------------------------------------------------------------------------- launches
@@ -953,7 +938,7 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
                    : tile_sizes_f<256>(format, ph.cfg, ph.bn, per_cu);
         const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
         const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
-        if (items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
+        if (rows * entries >= (int64_t)1 << 31 || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
             (double)items * n_kv * (double)tiles >= 2147483648.0) {
             fits = false;
             return;
@@ -995,13 +980,13 @@ static hipError_t launch_cfg(const AttnArgs &a, hipStream_t stream)
 template <int D>
 static hipError_t launch_join(const AttnArgs &a, hipStream_t stream)
 {
-    const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok * a.kv.n_kv * a.grp;
-    // Few rows can have many parts each: a block of eight waves per row while that does not need more
-    // than four blocks per CU, else a wave per row.
-    if (rows <= 1024)
-        hipLaunchKernelGGL((attn_join_kernel<D, 8>), dim3((unsigned)rows), dim3(512), 0, stream, a);
+    const int rows = a.b.n_batch * a.b.n_tok * a.grp, groups = 1024 / D;
+    // Few rows can have many parts each: a block per row while that is at most four blocks per CU.
+    if ((int64_t)rows * a.kv.n_kv <= 1024)
+        hipLaunchKernelGGL((attn_join_kernel<D, true>), dim3((unsigned)rows, (unsigned)a.kv.n_kv), dim3(256), 0, stream, a, rows);
     else
-        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)((rows + 7) / 8)), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((attn_join_kernel<D, false>), dim3((unsigned)((rows + groups - 1) / groups), (unsigned)a.kv.n_kv), dim3(256),
+                           0, stream, a, rows);
     return hipGetLastError();
 }
 
@@ -1016,7 +1001,7 @@ static hipError_t launch_attn_d(const AttnArgs &a, hipStream_t stream)
     };
     const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok;
     if (a.parent) {
-        hipLaunchKernelGGL(attn_ancestors_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(attn_ancestors_kernel, dim3((unsigned)a.b.n_batch), dim3(256), 0, stream, a);
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (a.prefix_pages) {
