@@ -223,7 +223,9 @@ struct AttnTile {
     static constexpr int ROWB = D * 2;                           // bytes of a row in LDS
     static constexpr int ES = DMA ? 2 : 1, CPR = D * ES / 16;    // 16-byte chunks of a cache row
     static constexpr int NCH = BN * CPR / THREADS;               // chunks of K (and of V) per thread
-    static constexpr int SWZ = (D / 8 < 16 ? D / 8 : 16) - 1;    // chunk c of row r lies at c ^ (r & SWZ)
+    // Chunk c of K's row r lies at c ^ (r & SWZ): an operand load takes one chunk of 16 rows.  V's lies at
+    // c ^ 2 (r & VSWZ): a transposing load takes two neighbouring chunks of 4 rows per 16 lanes.
+    static constexpr int SWZ = (D / 8 < 16 ? D / 8 : 16) - 1, VSWZ = SWZ / 2;
     static constexpr int buf_bytes = 2 * BN * ROWB, merge_bytes = NK > 1 ? BM * D * 4 : 0;
     static constexpr int tile_bytes = NB * buf_bytes > merge_bytes ? NB * buf_bytes : merge_bytes;
     static constexpr int sc_bytes = DMA ? 0 : 3 * BN * 4;        // k scale | log2 v scale | 1 / v scale
@@ -232,7 +234,7 @@ struct AttnTile {
                          o_ml = o_scan + (THREADS + 8) * 4, lds = o_ml + NK * BM * 4;
     static constexpr int waves = NR * NK;
     // workgroups per CU: by LDS, and eight waves (two per SIMD) where the registers allow that
-    static constexpr int by_lds = 160 * 1024 / lds, occ = D == 256 ? (!DMA && waves == 2 ? 1 : 2) : waves == 2 || RT == 2 ? 2 : waves == 4 && D == 128 ? 3 : 4;
+    static constexpr int by_lds = 160 * 1024 / lds, occ = D == 256 ? (waves == 2 ? 1 : 2) : waves == 2 || RT == 2 ? 2 : waves == 4 && D == 128 ? 3 : 4;
     static constexpr int by_waves = 4 * occ / waves, per_cu = by_lds < by_waves ? by_lds : by_waves;
     static_assert(KW % 32 == 0 && NCH >= 1 && BN * CPR % THREADS == 0 && BN <= 128, "tile");
     static_assert(DMA ? NB == 2 : 2 * BN <= THREADS, "staging");
@@ -348,25 +350,38 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                     pages = table[min(p0 + lane, last_page)];
                     absent = __ballot((uint32_t)pages >= (uint32_t)a.kv.n_pages);
                 }
-                gone_next = 0;
-#pragma unroll
-                for (int i = 0; i < BN / 16; ++i)
-                    gone_next |= (uint32_t)((absent >> ((min(kt * BN + 16 * i, it.limit - 1) >> a.kv.shift) - p0)) & 1) << i;
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    const int pg = page_of_run(kt * BN + pass_row(i));
-                    const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
-                    const int64_t at = row_of(in_pool ? pg : 0, kt * BN + pass_row(i)) * (D * TL::ES);
+                // pass i's rows start `at` bytes into k and v
+                const auto load = [&](int i, int64_t at) {
                     if constexpr (DMA) {
                         // LDS is written linearly: the swizzle is in the chunk each lane fetches
-                        const int r = pass_row(i) + lane / CPR, c = (lane % CPR) ^ (r & TL::SWZ);
+                        const int r = pass_row(i) + lane / CPR, c = lane % CPR;
                         unsigned char *to = lds + buf * TL::buf_bytes + pass_row(i) * TL::ROWB;
-                        const int64_t from = at + (lane / CPR) * TL::ROWB + 16 * c;
-                        lds_dma16(a.kv.k + from, to + 16 * lane);
-                        lds_dma16(a.kv.v + from, to + BN * TL::ROWB + 16 * lane);
+                        const int64_t from = at + (lane / CPR) * TL::ROWB;
+                        lds_dma16(a.kv.k + from + 16 * (c ^ (r & TL::SWZ)), to + 16 * lane);
+                        lds_dma16(a.kv.v + from + 16 * (c ^ (2 * (r & TL::VSWZ))), to + BN * TL::ROWB + 16 * lane);
                     } else {
                         kreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.k + at + 16 * lane);
                         vreg[i] = *reinterpret_cast<const u32x4_t *>(a.kv.v + at + 16 * lane);
+                    }
+                };
+                if ((1 << a.kv.shift) >= BN) {
+                    // the whole tile on one page: one address
+                    const int pg = page_of_run(kt * BN);
+                    const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
+                    gone_next = in_pool ? 0 : 0xffffffffu;
+                    const int64_t at = row_of(in_pool ? pg : 0, kt * BN) * (D * TL::ES);
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) load(i, at + pass_row(i) * (D * TL::ES));
+                } else {
+                    gone_next = 0;
+#pragma unroll
+                    for (int i = 0; i < BN / 16; ++i)
+                        gone_next |= (uint32_t)((absent >> ((min(kt * BN + 16 * i, it.limit - 1) >> a.kv.shift) - p0)) & 1) << i;
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) {
+                        const int pg = page_of_run(kt * BN + pass_row(i));
+                        const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
+                        load(i, row_of(in_pool ? pg : 0, kt * BN + pass_row(i)) * (D * TL::ES));
                     }
                 }
                 if constexpr (!DMA) {
@@ -396,13 +411,14 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 }
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    const int row = pass_row(i) + lane / CPR, c = lane % CPR, z = row & TL::SWZ;
+                    const int row = pass_row(i) + lane / CPR, c = lane % CPR;
+                    const int zk = row & TL::SWZ, zv = 2 * (row & TL::VSWZ);
                     const u32x4_t k = kreg[DMA ? 0 : i], v = vreg[DMA ? 0 : i];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int at = row * TL::ROWB + (((2 * c + e) ^ z) * 16);
-                        *reinterpret_cast<u32x4_t *>(kl + at) = widen_k<FMT>(k[2 * e], k[2 * e + 1]);
-                        *reinterpret_cast<u32x4_t *>(vl + at) = widen_v<FMT>(v[2 * e], v[2 * e + 1]);
+                        const int at = row * TL::ROWB, cc = 2 * c + e;
+                        *reinterpret_cast<u32x4_t *>(kl + at + 16 * (cc ^ zk)) = widen_k<FMT>(k[2 * e], k[2 * e + 1]);
+                        *reinterpret_cast<u32x4_t *>(vl + at + 16 * (cc ^ zv)) = widen_v<FMT>(v[2 * e], v[2 * e + 1]);
                     }
                 }
                 if (tid < 2 * BN) {
@@ -484,18 +500,20 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 const float *sc = reinterpret_cast<const float *>(lds + TL::o_sc + buf * TL::sc_bytes);
                 f4 s[RT][KB];
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) s[rt][kb] = f4{0.f, 0.f, 0.f, 0.f};
+                // the depth outermost: consecutive products go to different sums
 #pragma unroll
-                    for (int ks = 0; ks < D / 32; ++ks) {
+                for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
                         // row 16 kb + li of the wave's keys: its swizzle is li's alone
                         const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(
                             kl + (wk * KW + 16 * kb + li) * TL::ROWB + (((4 * ks + lg) ^ (li & TL::SWZ)) * 16));
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) s[rt][kb] = mfma_kq(kf, qf[rt][ks], s[rt][kb]);
                     }
-                }
                 float top[RT];
                 const auto maxima = [&](int kb) {
 #pragma unroll
@@ -577,7 +595,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 }
 #pragma unroll
                 for (int kp = 0; kp < KB / 2; ++kp) {
-                    const int r = 4 * lg + (li >> 2), z = r & TL::SWZ;  // row 32 kp + r, then 16 rows on
+                    const int r = 4 * lg + (li >> 2), z = 2 * (r & TL::VSWZ);  // row 32 kp + r, then 16 rows on
                     const unsigned char *base = vl + (wk * KW + 32 * kp + r) * TL::ROWB + (li & 1) * 8;
 #pragma unroll
                     for (int cb = 0; cb < D / 16; ++cb) {
@@ -897,7 +915,7 @@ static auto with_shape(int cfg, F f)
     case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
     case 1: return f(Shape<2, 2, 1, 64, bf16 ? 2 : 1>{});
     case 2: return f(Shape<4, 1, 1, 64, bf16 ? 2 : 1>{});
-    default: return f(Shape<D == 64 ? 4 : 8, 1, D == 64 ? 2 : 1, 64, 2>{});
+    default: return f(Shape<D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2, 64, 2>{});
     }
 }
 template <int D, int FMT>
