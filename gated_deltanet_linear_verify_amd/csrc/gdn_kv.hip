@@ -9,19 +9,30 @@
 
 namespace gdn {
 
-// max over the d / 8 lanes of a row (LPR = 8, 16 or 32 neighbouring lanes)
+// max over the d / 8 lanes of a row (LPR = 8, 16 or 32 neighbouring lanes), without LDS: within quads,
+// then mirrored halves of 8 and 16 lanes, then the two rows of 16.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v)
+{
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false));
+}
 template <int LPR>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v)
 {
-#pragma unroll
-    for (int m = 1; m < LPR; m *= 2) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+    v = dpp_umax<0xB1>(v);                       // quad_perm [1,0,3,2]
+    v = dpp_umax<0x4E>(v);                       // quad_perm [2,3,0,1]
+    v = dpp_umax<0x141>(v);                      // row_half_mirror
+    if constexpr (LPR >= 16) v = dpp_umax<0x140>(v);  // row_mirror
+    if constexpr (LPR == 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
     return v;
 }
 
-// One row's 8 channels of this lane into the cache.
-template <int FMT, int LPR>
+// One row's 8 channels of this lane into the cache; STREAM: past the caches (a prefill's rows, which
+// nothing reads soon: 46 us against 50 for 4 x 8191 tokens of 8 heads into i8).
+template <int FMT, int LPR, bool STREAM>
 __device__ __forceinline__ void write_codes(unsigned char *dst, float *scales, int64_t row, int li, bool live, const float (&x)[8])
 {
+#pragma clang fp contract(off)  // a code is the rounded product's, not the exact product's
     constexpr int d = 8 * LPR;
     if constexpr (FMT == kKvBf16) {
         if (live) store_row<8>(dst, row * d + 8 * li, true, x);
@@ -50,22 +61,27 @@ __device__ __forceinline__ void write_codes(unsigned char *dst, float *scales, i
             uint32_t c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
             w[q] = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
         } else {
-            w[q] = 0;
+            // |x (1 / s)| <= 127 (1 + 2^-22): adding 1.5 2^23 rounds to nearest, ties to even, and leaves
+            // the whole number in the low byte
+            uint32_t u[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int c = (int)fminf(fmaxf(rintf(y[j]), -127.0f), 127.0f);
-                w[q] |= (uint32_t)(c & 0xff) << (8 * j);
-            }
+            for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(y[j] + 12582912.0f);
+            w[q] = (u[0] & 0xff) | (u[1] & 0xff) << 8 | (u[2] & 0xff) << 16 | u[3] << 24;
         }
     }
     if (!live) return;
-    *reinterpret_cast<uint2 *>(dst + row * d + 8 * li) = make_uint2(w[0], w[1]);
+    const uint64_t codes = w[0] | (uint64_t)w[1] << 32;
+    uint64_t *to = reinterpret_cast<uint64_t *>(dst + row * d + 8 * li);
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(codes, to);
+    else
+        *to = codes;
     if (li == 0) scales[row] = scale;
 }
 
 // blockIdx.y: k rows of a group of heads, then v rows.  A thread keeps its 8 channels over the
 // group's heads, so a token's factors are formed once per group.
-template <int FMT, int LPR>
+template <int FMT, int LPR, int HB>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvRowsArgs a, int hpt, int groups)
 {
     const int li = threadIdx.x % LPR;
@@ -113,35 +129,42 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvRowsArgs a, int hpt, in
     const bool run8 = turn && !a.tab.interleaved && a.tab.pairs % 8 == 0;
     unsigned char *dst = is_v ? a.kv.v : a.kv.k;
     float *scales = is_v ? a.kv.vs : a.kv.ks;
-    for (int h = h0; h < min(h0 + hpt, a.kv.n_kv); ++h) {
-        float x[8];
+    // HB heads at a time, every load before the first store
+    for (int hb = h0; hb < min(h0 + hpt, a.kv.n_kv); hb += HB) {
+        float x[HB][8], y[HB][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-        if (live) {
+        for (int k = 0; k < HB; ++k) {
+            const int h = min(hb + k, a.kv.n_kv - 1);
             const int64_t at = rr * src.ld + h * src.hd;
-            load_row<8>(src.p, at + ch, src.bf16, x);
+            load_row<8>(src.p, at + ch, src.bf16, x[k]);
             if (turn) {
-                float y[8];
                 if (run8) {
-                    load_row<8>(src.p, at + mate[0], src.bf16, y);
+                    load_row<8>(src.p, at + mate[0], src.bf16, y[k]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float one[1];
                         load_row<1>(src.p, at + mate[j], src.bf16, one);
-                        y[j] = one[0];
+                        y[k][j] = one[0];
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (ch + j < a.tab.rot) x[j] = x[j] * c[j] + y[j] * s[j];
             }
         }
-        write_codes<FMT, LPR>(dst, scales, row0 + ((int64_t)h << a.kv.shift), li, live, x);
+#pragma unroll
+        for (int k = 0; k < HB; ++k) {
+            const int h = hb + k;
+            if (turn) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (ch + j < a.tab.rot) x[k][j] = x[k][j] * c[j] + y[k][j] * s[j];
+            }
+            write_codes<FMT, LPR, (HB > 1)>(dst, scales, row0 + ((int64_t)h << a.kv.shift), li, live && h < min(h0 + hpt, a.kv.n_kv), x[k]);
+        }
     }
 }
 
-template <int FMT, int LPR>
+// blockIdx.y: a group of HB heads, whose k and v rows a thread reads before it stores any.
+template <int FMT, int LPR, int HB>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvRowsArgs a)
 {
     constexpr int d = 8 * LPR;
@@ -153,36 +176,55 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvRowsArgs a)
     if (start < 0 || t >= kv_new(a.b, b)) return;
     const int64_t row0 = kv_row(a.kv, a.b, b, (int64_t)start + t, 0);
     if (row0 < 0) return;
-    const int h = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
-    const int64_t row = row0 + ((int64_t)h << a.kv.shift);
-    const unsigned char *src = is_v ? a.kv.v : a.kv.k;
-    const RowsView &out = is_v ? a.v : a.k;
-    float x[8];
-    if constexpr (FMT == kKvBf16) {
-        load_row<8>(src, row * d + 8 * li, true, x);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(src + row * d + 8 * li);
-        const float scale = (is_v ? a.kv.vs : a.kv.ks)[row];
-        const uint32_t ws[2] = {w.x, w.y};
+    const int h0 = blockIdx.y * HB;
+    uint4 code[2][HB];  // bf16: 8 values; 8 bits: 8 codes in x and y, the scale in z
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if constexpr (FMT == kKvE4m3) {
-                // byte j % 4 of the word; the builtin takes its index as a literal
-                float v = 0.0f;
-                switch (j % 4) {
-                case 0: v = __builtin_amdgcn_cvt_f32_fp8(ws[j / 4], 0); break;
-                case 1: v = __builtin_amdgcn_cvt_f32_fp8(ws[j / 4], 1); break;
-                case 2: v = __builtin_amdgcn_cvt_f32_fp8(ws[j / 4], 2); break;
-                default: v = __builtin_amdgcn_cvt_f32_fp8(ws[j / 4], 3); break;
-                }
-                x[j] = v * scale;
+    for (int k = 0; k < HB; ++k) {
+        const int64_t row = row0 + ((int64_t)min(h0 + k, a.kv.n_kv - 1) << a.kv.shift);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const unsigned char *src = w ? a.kv.v : a.kv.k;
+            if constexpr (FMT == kKvBf16) {
+                code[w][k] = *reinterpret_cast<const uint4 *>(src + (row * d + 8 * li) * 2);
             } else {
-                x[j] = (float)(int8_t)(ws[j / 4] >> (8 * (j % 4))) * scale;
+                const uint2 q = *reinterpret_cast<const uint2 *>(src + row * d + 8 * li);
+                code[w][k] = make_uint4(q.x, q.y, __float_as_uint((w ? a.kv.vs : a.kv.ks)[row]), 0);
             }
         }
     }
-    store_row<8>(out.p, r * out.ld + h * out.hd + 8 * li, out.bf16, x);
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+        if (h0 + k >= a.kv.n_kv) break;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const RowsView &out = w ? a.v : a.k;
+            const uint32_t q[4] = {code[w][k].x, code[w][k].y, code[w][k].z, code[w][k].w};
+            float x[8];
+            if constexpr (FMT == kKvBf16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = bf16_to_f32((uint16_t)(q[j / 2] >> (16 * (j % 2))));
+            } else {
+                const float scale = __uint_as_float(q[2]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float v;
+                    if constexpr (FMT == kKvE4m3) {
+                        // byte j % 4 of the word; the builtin takes its index as a literal
+                        switch (j % 4) {
+                        case 0: v = __builtin_amdgcn_cvt_f32_fp8(q[j / 4], 0); break;
+                        case 1: v = __builtin_amdgcn_cvt_f32_fp8(q[j / 4], 1); break;
+                        case 2: v = __builtin_amdgcn_cvt_f32_fp8(q[j / 4], 2); break;
+                        default: v = __builtin_amdgcn_cvt_f32_fp8(q[j / 4], 3); break;
+                        }
+                    } else {
+                        v = (float)(int8_t)(q[j / 4] >> (8 * (j % 4)));
+                    }
+                    x[j] = v * scale;
+                }
+            }
+            store_row<8>(out.p, r * out.ld + (h0 + k) * out.hd + 8 * li, out.bf16, x);
+        }
+    }
 }
 
 // One wave per (entry, head, k or v): lanes below the row's 16-byte chunks carry a chunk column
@@ -231,15 +273,23 @@ static hipError_t launch_rows(const KvRowsArgs &a, bool write, hipStream_t strea
 {
     const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok;
     const unsigned blocks = (unsigned)((rows + 256 / LPR - 1) / (256 / LPR));
+    // Four heads of a token per thread (a write: in batches of two, up to all heads, which share the rotary
+    // factors) once that leaves two waves per SIMD, else a thread per head: few tokens are latency.
+    // Writing 4 x 8191 tokens of 8 heads into i8: 86 us with a head per thread, 54 with four, 50 with all.
+    const int64_t threads = rows * LPR, two_waves = 256 * 4 * 2 * 64;
+    const bool four = threads * a.kv.n_kv / 4 >= two_waves && a.kv.n_kv > 1;
     if (write) {
-        // All heads of a token in one thread once that leaves four waves per SIMD, else a thread per
-        // head (few tokens: latency).
-        const int64_t threads = rows * LPR * 2;
-        const int hpt = threads >= 256 * 4 * 4 * 64 ? a.kv.n_kv : 1;
+        const int hpt = !four ? 1 : 2 * threads >= two_waves ? (a.kv.n_kv + 3) / 4 * 4 : 4;
         const int groups = (a.kv.n_kv + hpt - 1) / hpt;
-        hipLaunchKernelGGL((kv_write_kernel<FMT, LPR>), dim3(blocks, 2 * groups), dim3(256), 0, stream, a, hpt, groups);
+        const dim3 grid(blocks, 2 * groups);
+        if (four)
+            hipLaunchKernelGGL((kv_write_kernel<FMT, LPR, 2>), grid, dim3(256), 0, stream, a, hpt, groups);
+        else
+            hipLaunchKernelGGL((kv_write_kernel<FMT, LPR, 1>), grid, dim3(256), 0, stream, a, hpt, groups);
+    } else if (four) {
+        hipLaunchKernelGGL((kv_read_kernel<FMT, LPR, 4>), dim3(blocks, (a.kv.n_kv + 3) / 4), dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((kv_read_kernel<FMT, LPR>), dim3(blocks, 2 * a.kv.n_kv), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((kv_read_kernel<FMT, LPR, 1>), dim3(blocks, a.kv.n_kv), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }

@@ -12,7 +12,7 @@ namespace gdn {
 
 // Units of a (token, head): pairs / P groups of P pairs, then the channels past rot in groups of P
 // where out is another buffer.
-template <int P, int HPT>
+template <int P, int HPT, bool STREAM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units)
 {
     const uint32_t id = blockIdx.x * 256u + threadIdx.x;
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units)
         const RopeSeg &sg = a.seg[seg[k]];
         const int64_t at = t * sg.out.ld + head[k] * sg.out.hd;
         if (!turn) {
-            if (!sg.in_place) store_row<P>(sg.out.p, at + ca, sg.out.bf16, xa[k]);
+            if (!sg.in_place) store_row<P, STREAM>(sg.out.p, at + ca, sg.out.bf16, xa[k]);
             continue;
         }
         float ya[P], yb[P];
@@ -73,12 +73,12 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int units)
                 yb[j] = xa[k][j] * s[j] + xb[k][j] * c[j];
             }
         }
-        store_row<P>(sg.out.p, at + ca, sg.out.bf16, ya);
-        store_row<P>(sg.out.p, at + cb, sg.out.bf16, yb);
+        store_row<P, STREAM>(sg.out.p, at + ca, sg.out.bf16, ya);
+        store_row<P, STREAM>(sg.out.p, at + cb, sg.out.bf16, yb);
     }
 }
 
-template <int P, int HPT>
+template <int P, int HPT, bool STREAM>
 static hipError_t launch_rope_as(RopeArgs a, hipStream_t stream)
 {
     bool copies = false;
@@ -89,7 +89,7 @@ static hipError_t launch_rope_as(RopeArgs a, hipStream_t stream)
         a.t0 = t0;
         a.nt = a.n_tok - t0 < kTokensPerLaunch ? a.n_tok - t0 : kTokensPerLaunch;
         const dim3 grid((unsigned)(((int64_t)a.nt * units + 255) / 256), (unsigned)((a.heads + HPT - 1) / HPT));
-        hipLaunchKernelGGL((rope_kernel<P, HPT>), grid, dim3(256), 0, stream, a, units);
+        hipLaunchKernelGGL((rope_kernel<P, HPT, STREAM>), grid, dim3(256), 0, stream, a, units);
         if (hipError_t e = hipGetLastError()) return e;
         t0 += a.nt;
     }
@@ -99,7 +99,10 @@ static hipError_t launch_rope_as(RopeArgs a, hipStream_t stream)
 // Four pairs at a time where every run of four starts aligned (pairs and copied channels in whole
 // fours, strides multiples of four elements, and for interleaved runs of eight likewise: they are
 // read as two runs of four); single pairs otherwise.  Four heads per thread once that still leaves
-// four waves per SIMD (256 CUs x 4 x 4 x 64 threads); a few tokens get a thread per head.
+// two waves per SIMD (256 CUs x 4 x 2 x 64 threads); a few tokens get a thread per head (1024 tokens of
+// 40 heads, interleaved bf16 with YaRN: 7.4 us in a graph; 8191 tokens of 40 heads in fp32: 67 us with
+// four heads, 72 with eight).  Results past 64 MiB, twice the L2s, are stored past the caches (67 us
+// against 75, 336 MB at 5.0 TB/s).
 hipError_t launch_rope(const RopeArgs &a, hipStream_t stream)
 {
     bool four = a.tab.pairs % 4 == 0 && (a.d - a.tab.rot) % 4 == 0;
@@ -107,9 +110,14 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t stream)
         for (const RowsView *r : {&a.seg[s].x, &a.seg[s].out})
             four = four && r->ld % 4 == 0 && r->hd % 4 == 0 && (uintptr_t)r->p % (r->bf16 ? 8 : 16) == 0;
     const int64_t threads = (int64_t)a.n_tok * a.heads * (a.d / (four ? 8 : 2));
-    const bool share = threads / 4 >= 256 * 4 * 4 * 64;
-    if (four) return share ? launch_rope_as<4, 4>(a, stream) : launch_rope_as<4, 1>(a, stream);
-    return share ? launch_rope_as<1, 4>(a, stream) : launch_rope_as<1, 1>(a, stream);
+    const bool share = threads / 4 >= 256 * 4 * 2 * 64;
+    if (four) {
+        if (!share) return launch_rope_as<4, 1, false>(a, stream);
+        const int64_t values = (int64_t)a.n_tok * a.heads * a.d;
+        return values * (a.seg[0].out.bf16 ? 2 : 4) > (64 << 20) ? launch_rope_as<4, 4, true>(a, stream)
+                                                                : launch_rope_as<4, 4, false>(a, stream);
+    }
+    return share ? launch_rope_as<1, 4, false>(a, stream) : launch_rope_as<1, 1, false>(a, stream);
 }
 
 }  // namespace gdn

@@ -47,7 +47,17 @@ __device__ __forceinline__ void load_row(const void *p, int64_t i, bool bf16, fl
     }
 }
 
-template <int N>
+template <bool STREAM, class T, class V>
+__device__ __forceinline__ void put_row(T *p, V v)
+{
+    if constexpr (STREAM)
+        __builtin_nontemporal_store(v, reinterpret_cast<V *>(p));
+    else
+        *reinterpret_cast<V *>(p) = v;
+}
+
+// STREAM: vector stores past the caches, for rows that do not fit them.
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_row(void *p, int64_t i, bool bf16, const float (&x)[N])
 {
     if (bf16) {
@@ -56,12 +66,12 @@ __device__ __forceinline__ void store_row(void *p, int64_t i, bool bf16, const f
             bf16x8_t v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = (__bf16)x[j];
-            *reinterpret_cast<bf16x8_t *>(s) = v;
+            put_row<STREAM>(s, v);
         } else if constexpr (N == 4) {
             bf16x4_t v;
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = (__bf16)x[j];
-            *reinterpret_cast<bf16x4_t *>(s) = v;
+            put_row<STREAM>(s, v);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) s[j] = (__bf16)x[j];
@@ -74,7 +84,7 @@ __device__ __forceinline__ void store_row(void *p, int64_t i, bool bf16, const f
                 f4 v;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = x[4 * q + j];
-                *reinterpret_cast<f4 *>(s + 4 * q) = v;
+                put_row<STREAM>(s + 4 * q, v);
             }
         } else {
 #pragma unroll
