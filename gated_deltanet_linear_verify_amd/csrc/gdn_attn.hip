@@ -385,8 +385,11 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                     }
                 }
                 if constexpr (!DMA) {
-                    // all lanes: the pages are in lanes
-                    const int pg = __shfl(pages, (min(kt * BN + srow, it.limit - 1) >> a.kv.shift) - p0);
+                    int pg;
+                    if ((1 << a.kv.shift) >= BN)
+                        pg = page_of_run(kt * BN);
+                    else
+                        pg = __shfl(pages, (min(kt * BN + srow, it.limit - 1) >> a.kv.shift) - p0);  // in all lanes
                     const bool in_pool = (uint32_t)pg < (uint32_t)a.kv.n_pages;
                     if (tid < 2 * BN) {
                         sreg = (tid < BN ? a.kv.ks : a.kv.vs)[row_of(in_pool ? pg : 0, kt * BN + srow)];
@@ -898,10 +901,12 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 
 // -------------------------------------------------------------------------------------- launches
 
-// Tile shapes by the rows that share keys (attn_config): 16, 32, 64 or 128 rows.  with_shape
-// calls f with the shape's type.
-static int attn_config(int64_t rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
-constexpr int kAttnBm[4] = {16, 32, 64, 128};
+// Tile shapes by the rows that share keys (attn_config): 16, 32, 64, 128 or, at d 128, 256 rows.  with_shape
+// calls f with the shape's type.  Eight waves of 32 rows halve what 128-row tiles stage per row: 8 x 8.1k shared
+// keys under 8 x 6 rows of 4 heads in e4m3 165 -> 159 us, 8 trees of 64 nodes in i8 81 -> 78 us.  At d 256 a wave's
+// registers hold 16 rows, and at d 64 a tile's 8-bit codes are less than 16 bytes per thread.
+static int attn_config(int64_t rows, int d) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 || d != 128 ? 3 : 4; }
+constexpr int kAttnBm[5] = {16, 32, 64, 128, 256};
 
 template <int NR_, int NK_, int RT_, int BN_, int NB_>
 struct Shape {
@@ -915,7 +920,8 @@ static auto with_shape(int cfg, F f)
     case 0: return f(Shape<1, 2, 1, 64, bf16 ? 2 : 1>{});
     case 1: return f(Shape<2, 2, 1, 64, bf16 ? 2 : 1>{});
     case 2: return f(Shape<4, 1, 1, 64, bf16 ? 2 : 1>{});
-    default: return f(Shape<D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2, 64, 2>{});
+    case 3: return f(Shape<D == 256 ? 8 : 4, 1, D == 256 ? 1 : 2, 64, 2>{});
+    default: return f(Shape<D == 64 ? 4 : 8, 1, D == 256 ? 1 : 2, 64, 2>{});  // d 128 alone; else the type above
     }
 }
 template <int D, int FMT>
@@ -948,7 +954,7 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
     };
     bool fits = true;
     const auto phase = [&](AttnPhase &ph, int64_t rows, int entries, int64_t pages) {
-        ph.cfg = attn_config(rows);
+        ph.cfg = attn_config(rows, d);
         ph.bm = kAttnBm[ph.cfg];
         int per_cu = 1;
         d == 64 ? tile_sizes_f<64>(format, ph.cfg, ph.bn, per_cu)
