@@ -174,3 +174,41 @@ def block_step(d: dict, stream=None) -> None:
     gdn.gdn_linear(d["x"], d["w_in"], M, C + Z + 2 * Hv, hidden, segs, stream)
     verify(d, stream=stream)
     gdn.gdn_linear(d["out"], d["w_out"], M, hidden, Z, [(0, hidden, d["y"], hidden, 0)], stream)
+
+
+def upload_attention(inp: dict, rope: "gdn.gdn_rope_table", *, fmt: int, page_size: int, n_pages: int,
+                     prefix: bool = False) -> dict:
+    """Device tensors of one full-attention layer (workloads.make_attention_inputs): x [B*T][hidden], the
+    concatenated weight w_in [(n_q + 2 n_kv) d][hidden], the fused rows qkv [B*T][n_q + 2 n_kv][d] with the
+    views q, k and v of them, w_out, y, an empty cache of n_pages pages and the workspace.  The round's lists
+    (start, positions, parent, n_new, prefix_pages, prefix_len) are the caller's, as device tensors."""
+    B, T, hidden = inp["x"].shape
+    n_q, n_kv, hd = inp["n_q"], inp["n_kv"], inp["d"]
+    bf = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda().to(torch.bfloat16).contiguous()
+    d = {"B": B, "T": T, "hidden": hidden, "rope": rope, "scale": hd ** -0.5}
+    d["x"], d["w_in"], d["w_out"] = bf(inp["x"].reshape(B * T, hidden)), bf(inp["w_in"]), bf(inp["w_out"])
+    d["qkv"] = torch.empty((B * T, n_q + 2 * n_kv, hd), dtype=torch.bfloat16, device="cuda")
+    d["q"], d["k"], d["v"] = d["qkv"][:, :n_q], d["qkv"][:, n_q:n_q + n_kv], d["qkv"][:, n_q + n_kv:]
+    d["out"] = torch.empty((B * T, n_q, hd), dtype=torch.bfloat16, device="cuda")
+    d["y"] = torch.empty((B, T, hidden), dtype=torch.bfloat16, device="cuda")
+    dtype = {gdn.GDN_KV_BF16: torch.bfloat16, gdn.GDN_KV_E4M3: torch.float8_e4m3fn, gdn.GDN_KV_I8: torch.int8}[fmt]
+    k, v = (torch.zeros((n_pages, n_kv, page_size, hd), dtype=torch.uint8 if fmt else dtype, device="cuda").view(dtype)
+            for _ in range(2))
+    sc = [torch.zeros((n_pages, n_kv, page_size), dtype=torch.float32, device="cuda") for _ in range(2 if fmt else 0)]
+    d["kv"] = gdn.KvCache(k, v, *sc)
+    d["workspace"] = torch.empty(gdn.gdn_attn_workspace_bytes(d["kv"], n_q, B, T, prefix), dtype=torch.uint8, device="cuda")
+    return d
+
+
+def attention_step(d: dict, table, start, positions, n_new=None, parent=None, prefix_pages=None, prefix_len=None,
+                   stream=None) -> None:
+    """One full-attention layer over every drafted token: the q, k and v projections as one gdn_linear, q rotated in
+    place, k rotated on its way into the cache, gdn_attn_verify of the chain or tree, the output projection."""
+    B, T, kv, M = d["B"], d["T"], d["kv"], d["B"] * d["T"]
+    N, Z = d["w_in"].shape[0], d["w_out"].shape[1]
+    gdn.gdn_linear(d["x"], d["w_in"], M, N, d["hidden"], [(0, N, d["qkv"], N, 0)], stream)
+    gdn.gdn_rope(d["rope"], [(d["q"], d["q"])], positions, M, stream=stream)
+    gdn.gdn_kv_write(kv, d["k"], d["v"], table, start, n_new, B, T, rope=d["rope"], positions=positions, stream=stream)
+    gdn.gdn_attn_verify(kv, d["q"], table, start, n_new, parent, prefix_pages, prefix_len, d["out"], B, T, d["scale"],
+                        d["workspace"], stream=stream)
+    gdn.gdn_linear(d["out"], d["w_out"], M, d["hidden"], Z, [(0, d["hidden"], d["y"], d["hidden"], 0)], stream)

@@ -246,3 +246,23 @@ def make_block_inputs(shape: Shape, hidden: int, seed: int = 0) -> dict:
     inp["w_alpha"] = round_to(rng.normal(0.0, s_in, (Hv, hidden)), BF16)
     inp["w_out"] = round_to(rng.normal(0.0, s_out, (hidden, Hv * dv)), BF16)
     return inp
+
+
+def make_attention_inputs(n_batch: int, n_tok: int, hidden: int, n_q: int, n_kv: int, d: int, seed: int = 0) -> dict:
+    """Inputs of one full-attention layer call: x [B][T][hidden] ~ N(0, 1), w_in [(n_q + 2 n_kv) d][hidden] ~
+    N(0, 1/hidden) (the q, k and v projections, one output feature per row) and w_out [hidden][n_q d] ~
+    N(0, 1/(n_q d)), all bf16-rounded."""
+    rng = np.random.default_rng([seed, 2])
+    return {"n_q": n_q, "n_kv": n_kv, "d": d,
+            "x": round_to(rng.standard_normal((n_batch, n_tok, hidden)), BF16),
+            "w_in": round_to(rng.normal(0.0, 1.0 / np.sqrt(hidden), ((n_q + 2 * n_kv) * d, hidden)), BF16),
+            "w_out": round_to(rng.normal(0.0, 1.0 / np.sqrt(n_q * d), (hidden, n_q * d)), BF16)}
+
+
+def tree_path(parent: np.ndarray, node: int) -> list:
+    """The nodes from the root to ``node``: what accepting ``node`` keeps."""
+    path = []
+    while node >= 0:
+        path.append(int(node))
+        node = int(parent[node])
+    return path[::-1]

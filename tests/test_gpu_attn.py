@@ -307,3 +307,34 @@ def test_index_check_refuses():
         refused()
         t[at] = was
     assert torch.equal(c.run(), done)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_runs_longer_than_the_table_entries_at_hand(fmt, d):
+    """Contexts of 1250 pages, so many entries that a workgroup's run of key tiles crosses several hundred table
+    entries.  All entries name the same pages and ask the same."""
+    c = Case(fmt, d, 2, 1, 16, [20000], 1, seed=d).upload()
+    want, tol = c.want(0)
+    n = c.B = 96
+    c.g_table, c.g_ctx = c.g_table.repeat(n, 1), c.g_ctx.repeat(n)
+    c.g_q, c.out = c.g_q.repeat(n, 1, 1), torch.full((n, 2, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    c.ws = torch.full((gdn.gdn_attn_workspace_bytes(c.kv, 2, n, 1, False),), 0xff, dtype=torch.uint8, device="cuda")
+    got = c.run().double().cpu().numpy()
+    assert (np.abs(got - want) <= tol).all()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("shape", ["wide group", "more entries than threads", "more entries than threads, prefix",
+                                   "prefix of more rows than a tile", "largest page, odd context"])
+def test_sizes_at_the_edges(shape, fmt):
+    n_kv, grp, page, ctx, T, kw = {
+        "wide group": (1, 130, 16, [5, 100], 1, {}),
+        "more entries than threads": (1, 2, 16, [(7 * i) % 90 - 3 for i in range(700)], 1, {}),
+        "more entries than threads, prefix": (2, 1, 16, [(11 * i) % 40 for i in range(300)], 2,
+                                              dict(prefix=50, n_new=[i % 4 for i in range(300)])),
+        "prefix of more rows than a tile": (1, 4, 64, [(5 * i) % 70 for i in range(40)], 7, dict(prefix=130, tree=True)),
+        "largest page, odd context": (2, 2, 4096, [4095, 4096, 1], 3, {}),
+    }[shape]
+    c = Case(fmt, 128, n_kv, grp, page, ctx, T, seed=len(shape), **kw).upload()
+    say(f"{shape}, {fmt}: {c.check(c.run()):.2f} of the bound")
