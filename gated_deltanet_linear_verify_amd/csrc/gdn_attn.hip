@@ -26,8 +26,9 @@
 // exactly.  The k scale multiplies the scores; the v scale is folded into the exponent, w_j =
 // 2^(s_j + log2 vs_j - m) with m the maximum of that sum, so the largest weight is 1 whatever the
 // scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's own sum takes w_j / vs_j in
-// fp32.  (That holds while the v scales of the keys a workgroup meets lie within 2^100 of each other;
-// a scale of 0 goes with codes of 0 and counts as 1.)
+// fp32.  (That holds while the v scales of the keys a workgroup meets lie within 2^100 of each other; one
+// below 2^-64 counts as that, which moves an output by at most 448 2^-64, and 0, which goes with codes of
+// 0, as 1.)
 #include <algorithm>
 #include <type_traits>
 
@@ -433,7 +434,8 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                             sreg = 0.0f;
                             *bad = 1;
                         }
-                        const float vs = sreg == 0.0f ? 1.0f : sreg;
+                        // 2^-64 at least: 1 / vs and the sums of w / vs stay finite (a NaN stays one)
+                        const float vs = sreg == 0.0f ? 1.0f : sreg < 0x1p-64f ? 0x1p-64f : sreg;
                         sc[BN + srow] = __builtin_amdgcn_logf(vs);  // base 2
                         sc[2 * BN + srow] = 1.0f / vs;
                     }
@@ -962,7 +964,7 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
                    : tile_sizes_f<256>(format, ph.cfg, ph.bn, per_cu);
         const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
         const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
-        if (rows * entries >= (int64_t)1 << 31 || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
+        if (rows * entries > kMaxTokenRows || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
             (double)items * n_kv * (double)tiles >= 2147483648.0) {
             fits = false;
             return;

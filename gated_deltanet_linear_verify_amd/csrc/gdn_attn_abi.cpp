@@ -59,7 +59,7 @@ GDN_API size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n
 {
     const char *fn = "gdn_attn_workspace_bytes";
     if (gdn::abi_check_kv(fn, kv, false) || check_heads(fn, kv, n_q)) return 0;
-    if (n_batch < 1 || n_batch > 65535 || n_tok < 1 || (int64_t)n_batch * n_tok > (int64_t)1 << 30) {
+    if (n_batch < 1 || n_batch > 65535 || n_tok < 1 || (int64_t)n_batch * n_tok > gdn::kMaxTokenRows) {
         abi_fail(GDN_ERR_SHAPE, "%s: n_batch or n_tok out of range", fn);
         return 0;
     }
@@ -82,8 +82,9 @@ GDN_API int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const i
     if (int r = check_heads(fn, kv, q->n_heads)) return r;
     if (int r = gdn::abi_check_rows(fn, "q", q, q->n_heads)) return r;
     if (int r = gdn::abi_check_rows(fn, "out", out, q->n_heads)) return r;
+    if (int r = gdn::abi_check_apart(fn, "out", out, (int64_t)batch->n_batch * batch->n_tok, kv->d)) return r;
     if (q->dtype != GDN_BF16 || out->dtype != GDN_BF16) return abi_fail(GDN_ERR_DTYPE, "%s: q and out must be GDN_BF16", fn);
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return abi_fail(GDN_ERR_ARG, "%s: scale must be finite and > 0", fn);
+    if (!(scale > 0.0f) || !std::isfinite(scale * gdn::kLog2E)) return abi_fail(GDN_ERR_ARG, "%s: scale must be finite and > 0", fn);
     if (parent && batch->n_tok > kMaxTreeNodes)
         return abi_fail(GDN_ERR_SHAPE, "%s: a tree of %d nodes, at most %d", fn, batch->n_tok, kMaxTreeNodes);
     if ((prefix_pages != nullptr) != (prefix_len != nullptr))
@@ -112,7 +113,7 @@ GDN_API int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const i
     a.b = gdn::kv_batch_view(*batch);
     a.q = gdn::rows_view(*q);
     a.out = gdn::rows_view(*out);
-    a.scale = scale * 1.44269504088896341f;
+    a.scale = scale * gdn::kLog2E;
     a.parent = parent;
     a.prefix_pages = prefix_pages;
     a.prefix_len = prefix_len;

@@ -122,6 +122,7 @@ hipError_t launch_linear(const LinearArgs &a, hipStream_t stream);
 // ---- full-attention layers: rotary positions, paged KV cache, attention ----
 
 // gdn_rope_table as the kernels take it (by value).
+constexpr float kLog2E = 1.44269504088896341f;
 constexpr int kMaxRopePairs = 128;
 struct RopeTab {
     int32_t rot, pairs, interleaved, n_axes;
@@ -177,6 +178,10 @@ struct KvCommitArgs {
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t stream);
 // Attention of drafted tokens (gdn_attn.hip).  A launch's work is a list of items, each a tile of query
 // rows of one KV head with the keys they see; AttnPhase describes one launch's items.
+// Token rows of a call (for attention: times the query heads of a group): 2^26 rows of 32 lanes, or the
+// join's of 64, stay below the 2^32 threads of a launch's x axis.
+constexpr int64_t kMaxTokenRows = (int64_t)1 << 26;
+
 struct AttnPhase {
     int32_t cfg;        // tile shape, by rows (attn_config)
     int32_t bm, bn;     // rows and keys of a tile
@@ -210,6 +215,7 @@ hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
 // Checks shared by the cache's entry points (gdn_kv_abi.cpp); each sets the last error.
 int abi_check_kv(const char *fn, const gdn_kv *kv, bool pointers);
 int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_heads);  // aligned rows
+int abi_check_apart(const char *fn, const char *what, const gdn_rows *r, int64_t n_rows, int d);  // rows to write do not overlap
 int abi_check_batch(const char *fn, const gdn_kv_batch *b);
 // Under GDN_F_CHECK_INDICES: the batch's arrays, copied to the host, name places that exist, for
 // positions [0, start + n) (from_zero) or [start, start + n).

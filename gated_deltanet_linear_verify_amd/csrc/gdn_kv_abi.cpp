@@ -100,6 +100,13 @@ int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_he
     return GDN_OK;
 }
 
+int abi_check_apart(const char *fn, const char *what, const gdn_rows *r, int64_t n_rows, int d)
+{
+    if ((n_rows > 1 && r->ld > -d && r->ld < d) || (r->n_heads > 1 && r->hd > -d && r->hd < d))
+        return abi_fail(GDN_ERR_ARG, "%s: %s: rows or heads that are written lie on top of each other", fn, what);
+    return GDN_OK;
+}
+
 int abi_check_batch(const char *fn, const gdn_kv_batch *b)
 {
     if (!b || !b->block_table || !b->start)
@@ -107,8 +114,8 @@ int abi_check_batch(const char *fn, const gdn_kv_batch *b)
     if (b->n_batch < 1 || b->n_batch > 65535) return abi_fail(GDN_ERR_RANGE, "%s: n_batch %d outside [1, 65535]", fn, b->n_batch);
     if (b->n_tok < 1) return abi_fail(GDN_ERR_RANGE, "%s: n_tok must be >= 1", fn);
     if (b->max_pages < 1) return abi_fail(GDN_ERR_SHAPE, "%s: max_pages must be >= 1", fn);
-    if ((int64_t)b->n_batch * b->n_tok > (int64_t)1 << 30)
-        return abi_fail(GDN_ERR_SHAPE, "%s: more than 2^30 token rows", fn);
+    if ((int64_t)b->n_batch * b->n_tok > kMaxTokenRows)
+        return abi_fail(GDN_ERR_SHAPE, "%s: more than 2^26 token rows", fn);
     return GDN_OK;
 }
 
@@ -241,6 +248,7 @@ GDN_API int gdn_rope(const gdn_rope_table *table, const gdn_rows *x, const gdn_r
         }
         if (x[s].n_heads < 1 || x[s].n_heads > 8192 || out[s].n_heads != x[s].n_heads)
             return abi_fail(GDN_ERR_SHAPE, "%s: segment %d: %d heads in, %d out", fn, s, x[s].n_heads, out[s].n_heads);
+        if (int r = gdn::abi_check_apart(fn, "out", &out[s], n_tok, d)) return r;
         const bool same = x[s].ptr == out[s].ptr;
         if (same && (x[s].ld != out[s].ld || x[s].hd != out[s].hd || x[s].dtype != out[s].dtype))
             return abi_fail(GDN_ERR_ARG, "%s: segment %d is in place with other strides or another dtype", fn, s);
@@ -270,6 +278,11 @@ static int kv_rows(const char *fn, bool write, const gdn_kv *kv, const gdn_kv_ba
     if (int r = gdn::abi_check_rows(fn, "k", k, kv->n_kv)) return r;
     if (int r = gdn::abi_check_rows(fn, "v", v, kv->n_kv)) return r;
     if (write && k->dtype != v->dtype) return abi_fail(GDN_ERR_DTYPE, "%s: k and v must have one dtype", fn);
+    if (!write) {
+        const int64_t rows = (int64_t)batch->n_batch * batch->n_tok;
+        if (int r = gdn::abi_check_apart(fn, "k", k, rows, kv->d)) return r;
+        if (int r = gdn::abi_check_apart(fn, "v", v, rows, kv->d)) return r;
+    }
     gdn::KvRowsArgs a{};
     if (rope) {
         if (!positions) return abi_fail(GDN_ERR_ARG, "%s: a rope table without positions", fn);

@@ -402,7 +402,8 @@ int gdn_linear(const void *x, const void *w, int32_t M, int32_t N, int32_t K, co
  *
  * gdn_rows names per-token rows of heads: the d channels of head h of token t start at
  * ptr + (t * ld + h * hd) elements, contiguous; ld and hd may be any strides, so q, k and v may
- * stay inside the fused rows that one projection wrote.
+ * stay inside the fused rows that one projection wrote.  Rows that are read may repeat (a stride of
+ * 0); rows that are written must not overlap, and strides of less than d there are GDN_ERR_ARG.
  */
 typedef struct gdn_rows {
     void *ptr;
@@ -463,8 +464,8 @@ int gdn_rope_init(const gdn_rope_params *params, gdn_rope_table *table);
  * rot_dim to d are copied.  Angles are formed and reduced in 64 bits, so far positions lose nothing;
  * the rotation is in 32 bits, rounded once.  positions: device int32 [n_axes][n_tok], any value.
  * x[s] and out[s]: rows of d channels (rot_dim <= d <= 256) with equal n_heads; in place if they
- * name the same memory with the same strides and type, otherwise they must not overlap.  Types of x
- * and out may differ.  n_tok == 0 is a no-op (positions and ptr may then be NULL).  Errors: NULL ->
+ * name the same memory with the same strides and type, otherwise they must not overlap, nor may one
+ * segment's out and another segment's rows.  Types of x and out may differ.  n_tok == 0 is a no-op (positions and ptr may then be NULL).  Errors: NULL ->
  * GDN_ERR_ARG; n_segs, n_heads (1 .. 8192) or d out of range -> GDN_ERR_SHAPE; n_tok < 0 ->
  * GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE; same pointer with other strides or types, a pointer not
  * aligned to its elements, a table that gdn_rope_init did not make -> GDN_ERR_ARG.
@@ -477,8 +478,8 @@ int gdn_rope(const gdn_rope_table *table, const gdn_rows *x, const gdn_rows *out
  * held in 8 bits).  k and v are [n_pages][n_kv][page_size][d] of the format's elements, 16-byte
  * aligned; the 8-bit formats keep one fp32 scale per token and head, k_scale and v_scale
  * [n_pages][n_kv][page_size] (NULL for GDN_KV_BF16): value = code * scale, scale = max |x| / 448
- * (e4m3) or / 127 (i8), code = x * (1 / scale) rounded to nearest, ties to even.  A row of zeros has
- * scale 0.  A row that holds an infinity or a NaN gets codes 0 and scale NaN, so that every value of
+ * (e4m3) or / 127 (i8), code = x * (1 / scale) rounded to nearest, ties to even.  A row of zeros, or of
+ * values so small that 1 / scale overflows, has codes and scale 0.  A row that holds an infinity or a NaN gets codes 0 and scale NaN, so that every value of
  * it reads back as NaN.  flags: GDN_F_CHECK_INDICES or 0.
  */
 enum gdn_kv_format { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1, GDN_KV_I8 = 2 };
@@ -506,7 +507,7 @@ size_t gdn_kv_bytes(const gdn_kv *kv, size_t *scale_bytes);
  * whose page is outside [0, n_pages): nothing is read or written there; rows of tokens that do not count
  * are left as they were.  With GDN_F_CHECK_INDICES in kv->flags the host copies the arrays back
  * (synchronously) and returns GDN_ERR_RANGE for any of these before launching; on a capturing
- * stream that is GDN_ERR_ARG.  n_batch 1 .. 65535, n_tok >= 1.
+ * stream that is GDN_ERR_ARG.  n_batch 1 .. 65535, n_tok >= 1, n_batch * n_tok <= 2^26.
  */
 typedef struct gdn_kv_batch {
     const int32_t *block_table;
@@ -551,15 +552,17 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  * pages prefix_pages (device int32 [max_prefix_pages]): a prefix that all share, held once, and
  * scored for the rows of all entries together, so its pages are read once for the batch.
  *   out = sum_j softmax_j(scale q . k_j) v_j,  query head h reading KV head h / (n_q / n_kv).
- * Scores, maxima and sums are in fp32, the weights are rounded to bf16 for the product with v.  A
- * key that a row does not see does not reach it, whatever its k and v hold.  A row whose keys are
- * all on pages outside the pool is zero.
+ * Scores, maxima and sums are in fp32; for the product with v the weights are rounded to bf16 (bf16
+ * cache) or fp16 (8 bits).  A key that a row does not see does not reach it, whatever its k and v
+ * hold.  A row whose keys are all on pages outside the pool is zero.  Scales of an 8-bit cache are not
+ * negative; a v scale of 0 goes with codes of 0, one below 2^-64 counts as 2^-64, and those of the
+ * keys of a call lie within 2^100 of each other.
  *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
- *   gdn_kv_write.  scale: finite, > 0.
+ *   gdn_kv_write; out may be q itself.  scale: > 0, scale log2(e) finite in fp32.
  *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
  *   calls (and recorded graphs) that may run at the same time need one each.
  * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, or a bad scale ->
- * GDN_ERR_ARG; sizes whose tiles would pass 2^31 -> GDN_ERR_SHAPE.
+ * GDN_ERR_ARG; sizes whose key tiles would pass 2^31, or n_batch n_tok n_q / n_kv > 2^26 -> GDN_ERR_SHAPE.
  */
 int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *parent,
                     const int32_t *prefix_pages, int32_t max_prefix_pages, const int32_t *prefix_len,

@@ -165,3 +165,33 @@ def test_attn_workspace(L):
     n = lambda n_q, b, t, p, **kw: L.gdn_attn_workspace_bytes(ctypes.byref(_kv(**kw)), n_q, b, t, p)  # noqa: E731
     assert 0 < n(32, 64, 16, 0) < n(32, 64, 16, 1)
     assert n(6, 1, 1, 0) == n(32, 0, 1, 0) == n(32, 1, 0, 0) == n(32, 70000, 1, 0) == n(32, 1, 1, 0, d=96) == 0
+
+
+def test_refuses_outputs_on_top_of_each_other(L):
+    """A broadcast row may be read, never written."""
+    t = gdn.gdn_rope_init(64)
+    ok, flat, heads, back = _rows(), _rows(ptr=2 * FAKE, ld=0), _rows(ptr=2 * FAKE, hd=64), _rows(ptr=2 * FAKE, ld=-64)
+    ref_, kv, b = ctypes.byref, _kv(), _batch()
+    for bad in (flat, heads, back):
+        assert L.gdn_rope(ref_(t), ref_(ok), ref_(bad), 1, 128, FAKE, 3, 0, None) == gdn.GDN_ERR_ARG
+        assert L.gdn_kv_read(ref_(kv), ref_(b), ref_(bad), ref_(ok), None) == gdn.GDN_ERR_ARG
+        assert L.gdn_kv_read(ref_(kv), ref_(b), ref_(ok), ref_(bad), None) == gdn.GDN_ERR_ARG
+        assert L.gdn_attn_verify(ref_(kv), ref_(b), None, None, 0, None, ref_(ok), ref_(bad), 0.1, FAKE, 1 << 40, None) == gdn.GDN_ERR_ARG
+
+
+def test_refuses_more_rows_than_a_launch_holds(L):
+    b, r, kv = _batch(n_batch=60000, n_tok=1119), ctypes.byref(_rows()), ctypes.byref(_kv())  # just over 2^26
+    assert L.gdn_kv_write(kv, ctypes.byref(b), r, r, None, None, None) == gdn.GDN_ERR_SHAPE
+    assert L.gdn_kv_read(kv, ctypes.byref(b), r, r, None) == gdn.GDN_ERR_SHAPE
+    n = lambda n_q, b, t: L.gdn_attn_workspace_bytes(kv, n_q, b, t, 0)  # noqa: E731
+    assert n(4, 60000, 1118) and not n(4, 60000, 1119) and not n(8, 60000, 1118)
+    wide = _batch(n_batch=60000, n_tok=1118)
+    assert L.gdn_attn_verify(kv, ctypes.byref(wide), None, None, 0, None, ctypes.byref(_rows(n_heads=8, ld=1024)),
+                             ctypes.byref(_rows(n_heads=8, ld=1024)), 0.1, FAKE, 1 << 62, None) == gdn.GDN_ERR_SHAPE
+
+
+def test_refuses_a_scale_that_overflows(L):
+    r = ctypes.byref(_rows())
+    for scale in (3e38, -1.0):
+        assert L.gdn_attn_verify(ctypes.byref(_kv()), ctypes.byref(_batch()), None, None, 0, None, r, r, scale, FAKE, 1 << 40,
+                                 None) == gdn.GDN_ERR_ARG

@@ -338,3 +338,27 @@ def test_sizes_at_the_edges(shape, fmt):
     }[shape]
     c = Case(fmt, 128, n_kv, grp, page, ctx, T, seed=len(shape), **kw).upload()
     say(f"{shape}, {fmt}: {c.check(c.run()):.2f} of the bound")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+@pytest.mark.parametrize("small", [0.0, 1e-42, 3e-39, 1e-20])
+def test_very_small_scales(fmt, small):
+    """v scales far below the others', down to subnormal ones, for some keys and for all: below 2^-64 they count as
+    2^-64, which moves a row of at most 448 by 448 2^-64 at most; nothing becomes infinite or NaN."""
+    for every in (3, 1):
+        c = Case(fmt, 128, 2, 4, 16, [100, 40], 3, seed=17)
+        c.store["v_scale"][:, :, ::every] = small
+        c.store["k_scale"][:, :, 1::5] = small
+        c.store["v"].view(torch.uint8)[:, :, ::every] &= 0xff if small else 0
+        c.upload()
+        got = c.run().double().cpu().numpy().reshape(2, 3, 8, 128)
+        for b in range(2):
+            want, tol = c.want(b)
+            assert (np.abs(got[b] - want) <= tol + 448 * 2.0 ** -64).all(), (every, b)
+
+
+def test_output_in_place_of_q():
+    c = Case("bf16", 128, 2, 4, 16, [100, 40, 3000], 3, seed=5).upload()
+    want = c.run().clone()
+    q = c.g_q.clone()
+    assert torch.equal(c.run(q=q, out=q), want)
