@@ -41,6 +41,7 @@ typedef unsigned long long u64x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 8.0f;  // weights reach 2^8 where fp16 ends at 2^16
 
 __device__ __forceinline__ f4 mfma_kq(bf16x8_t a, bf16x8_t b, f4 c)
 {
@@ -531,12 +532,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
                     const int k0 = wk * KW + 16 * kb + 4 * lg;  // the lane's four keys of the block
-                    if constexpr (DMA) {
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) s[rt][kb][i] *= a.scale;
-                    } else {
+                    if constexpr (!DMA) {  // bf16: the scale is applied on the way into the exponent
                         const f4 c = *reinterpret_cast<const f4 *>(sc + k0), lv = *reinterpret_cast<const f4 *>(sc + BN + k0);
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt)
@@ -561,16 +557,19 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         maxima(kb);
                     }
                 }
+                // The maximum is let grow by kSlack before it is taken over and the sums are rescaled (64 to 128
+                // multiplications): any stand-in serves that keeps the weights in range.  With scores in no
+                // order the true one grows in every second tile of a hundred for some row of a wave's 32.
                 bool grew = false;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    top[rt] = quad_max(top[rt]);
-                    grew |= top[rt] > m[rt];
+                    if constexpr (DMA) top[rt] *= a.scale;
+                    grew |= top[rt] - m[rt] > kSlack;  // from -inf as well
                 }
                 if (__any(grew)) {
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
-                        const float mn = fmaxf(m[rt], top[rt]), f = exp2_f(m[rt] - finite_max(mn));
+                        const float mn = fmaxf(m[rt], quad_max(top[rt])), f = exp2_f(m[rt] - finite_max(mn));
                         m[rt] = mn;
                         l[rt] *= f;
 #pragma unroll
@@ -589,7 +588,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         const float mf = finite_max(m[rt]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float w = exp2_f(s[rt][kb][i] - mf);
+                            const float w = exp2_f(DMA ? __builtin_fmaf(s[rt][kb][i], a.scale, -mf) : s[rt][kb][i] - mf);
                             if constexpr (DMA)
                                 l[rt] += w;
                             else

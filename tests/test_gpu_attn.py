@@ -362,3 +362,24 @@ def test_output_in_place_of_q():
     want = c.run().clone()
     q = c.g_q.clone()
     assert torch.equal(c.run(q=q, out=q), want)
+
+
+@pytest.mark.parametrize("slope", [2.0, 7.0, 25.0, -7.0])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_scores_that_keep_growing(fmt, slope):
+    """Scores that rise (or fall) by a steady amount per 64 keys, in powers of two, below and above what the running
+    maximum is let grow by before the sums are rescaled."""
+    c = Case(fmt, 128, 1, 4, 64, [1500, 700], 4, seed=31, prefix=650)
+    u = torch.from_numpy(np.sign(c.rng.standard_normal(128)))
+    for pages, n in ((c.shared, 650), (c.table[0], 1504), (c.table[1], 704)):
+        pos = np.arange(n)
+        pg, at = c.at(pages, pos)
+        up = torch.from_numpy(pos if slope > 0 else n - pos) * (abs(slope) / 64 * np.log(2) / 128 ** 0.5)  # times u . u = 128
+        if fmt == "bf16":
+            c.store["k"][pg, 0, at] = (up[:, None] * u).to(torch.bfloat16)
+        else:
+            c.store["k"].view(torch.uint8)[pg, 0, at] = (u * 3).to(FMT[fmt]).view(torch.uint8)
+            c.store["k_scale"][pg, 0, at] = (up / 3).float()
+    c.q = (u + torch.from_numpy(c.rng.standard_normal((8, 4, 128)) * 0.01)).to(torch.bfloat16)
+    c.upload()
+    say(f"slope {slope}, {fmt}: {c.check(c.run()):.2f} of the bound")
