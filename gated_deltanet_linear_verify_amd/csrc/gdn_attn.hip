@@ -29,6 +29,15 @@
 // fp32.  (That holds while the v scales of the keys a workgroup meets lie within 2^100 of each other; one
 // below 2^-64 counts as that, which moves an output by at most 448 2^-64, and 0, which goes with codes of
 // 0, as 1.)
+//
+// What bounds it.  Few rows per key: the cache's bytes (64 tokens over 50 .. 20000 keys each, 8 heads, e4m3:
+// 1.35 GB in 245 us, 5.5 TB/s, as fast as a large copy).  Many rows per key: a tile's LDS reads (32 KB per wave
+// and tile), its softmax (240 vector instructions beside 64 MFMA at d 128 and 32 rows per wave) and its MFMA
+// follow one another in a wave, and two waves per SIMD, which is what the registers hold, overlap them only in
+// part: 8.1k shared keys under 64 x 16 rows (half of them there) of 32 heads in e4m3, 72 GFLOP, 115 us, 0.63
+// PFLOP/s of 1.40; the vector unit issues in 56% of the time, the matrix unit is busy in 34%.  A wave of 32 rows
+// at d <= 128 reads half the LDS bytes per row of one of 16 (the same call: 195 -> 174 us).  One token: latency
+// (11 us), a chain of three dependent loads (lengths, page, rows) and the joins between the key waves.
 #include <algorithm>
 #include <type_traits>
 
@@ -559,7 +568,8 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 }
                 // The maximum is let grow by kSlack before it is taken over and the sums are rescaled (64 to 128
                 // multiplications): any stand-in serves that keeps the weights in range.  With scores in no
-                // order the true one grows in every second tile of a hundred for some row of a wave's 32.
+                // order the true one grows in every second tile of a hundred for some row of a wave's 32 (8.1k
+                // shared keys as above 158 -> 150 us, trees 79 -> 75 us).
                 bool grew = false;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
@@ -816,7 +826,9 @@ __device__ __forceinline__ Parts attn_parts(const AttnPhase &ph, const Item &it,
 // Rows of the result from their parts.  D / 4 threads take a row, four channels each; with SPLIT the
 // block's groups of that many threads share one row (few rows can have many parts: long contexts),
 // otherwise each has its own.  What a row has to look up (its lengths, its place in the prefix's rows,
-// its items' first units) is read before any of it is used: one wait instead of a chain of them.
+// its items' first units) is read before any of it is used: one wait instead of a chain of them (37 -> 20 us
+// beside the shared prefix of 8.1k; eight rows per wave that looked them up once were no faster, and slower
+// by 25 us where a row has eight parts).
 template <int D, bool SPLIT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
@@ -902,10 +914,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 
 // -------------------------------------------------------------------------------------- launches
 
-// Tile shapes by the rows that share keys (attn_config): 16, 32, 64, 128 or, at d 128, 256 rows.  with_shape
-// calls f with the shape's type.  Eight waves of 32 rows halve what 128-row tiles stage per row: 8 x 8.1k shared
-// keys under 8 x 6 rows of 4 heads in e4m3 165 -> 159 us, 8 trees of 64 nodes in i8 81 -> 78 us.  At d 256 a wave's
-// registers hold 16 rows, and at d 64 a tile's 8-bit codes are less than 16 bytes per thread.
+// Tile shapes by the rows that share keys (attn_config): the smallest of 16, 32, 64, 128 and, at d 128, 256 rows
+// that holds them.  32 entries of 1000 .. 4000 keys, 8 heads, us with that shape (with the next smaller, the next
+// larger one):
+//    rows             16             32             64              128              256
+//    e4m3, d 128   50 (-, 53)   57 (69, 62)    69 (85, 90)    103 (111, 150)    169 (177, -)
+//    bf16, d 128   75 (-, 76)   83 (111, 82)   92 (118, 93)   107 (132, 130)    151 (164, -)
+//    bf16, d 256  149 (-, 146) 160 (272, 168) 181 (287, 185)  204 (332, -)
+// Eight waves of 32 rows halve what 128-row tiles stage per row.  At d 256 a wave's registers hold 16 rows (32 in
+// four waves of 512 registers: 32.7k shared keys 128 -> 180 us), and at d 64 a tile's 8-bit codes are less than
+// 16 bytes per thread.  with_shape calls f with the shape's type.
 static int attn_config(int64_t rows, int d) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 || d != 128 ? 3 : 4; }
 constexpr int kAttnBm[5] = {16, 32, 64, 128, 256};
 
