@@ -20,15 +20,17 @@
 // operand registers without leaving the lane (the key order inside a 32-deep step is permuted alike
 // on both operands).
 //
-// Formats.  A bf16 cache goes into LDS as it is (global_load_lds), its weights are rounded to bf16 for
-// the second product: half a step is 2^-9 .. 2^-8 of a weight, which averages over the keys.  8-bit
-// codes travel through registers and are widened on the way into LDS, k to bf16 and v to fp16, both
-// exactly.  The k scale multiplies the scores; the v scale is folded into the exponent, w_j =
-// 2^(s_j + log2 vs_j - m) with m the maximum of that sum, so the largest weight is 1 whatever the
-// scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's own sum takes w_j / vs_j in
-// fp32.  (That holds while the v scales of the keys a workgroup meets lie within 2^100 of each other; one
-// below 2^-64 counts as that, which moves an output by at most 448 2^-64, and 0, which goes with codes of
-// 0, as 1.)
+// Formats.  A bf16 cache goes into LDS as it is (global_load_lds), and the second product takes its
+// weights in bf16: in two parts (2^-17 of a weight is lost) in tiles of up to 64 rows, which the cache's
+// bytes bound (32 entries of 1000 .. 4000 keys, 16 to 64 rows: d 128 + 0 .. 1%, d 256 + 2 .. 4%), in one
+// beyond, where the second part's products would cost 5 .. 22% (128 and 256 rows) for an error of 2^-9 of a
+// weight, rms, beside the 2^-9 of the stored result.  8-bit codes travel through registers and are widened on
+// the way into LDS, k to bf16 and v to fp16, both exactly.  The k scale multiplies the scores; the v scale is
+// folded into the exponent, w_j = 2^(s_j + log2 vs_j - m) with m the maximum of that sum (or up to 8 below it),
+// so no weight passes 2^8 whatever the scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's
+// own sum takes w_j / vs_j in fp32.  (That holds while the v scales of the keys a workgroup meets lie within
+// 2^100 of each other; one below 2^-64 counts as that, which moves an output by at most 448 2^-64, and 0, which
+// goes with codes of 0, as 1.)
 //
 // What bounds it.  Few rows per key: the cache's bytes (64 tokens over 50 .. 20000 keys each, 8 heads, e4m3:
 // 1.35 GB in 245 us, 5.5 TB/s, as fast as a large copy).  Many rows per key: a tile's LDS reads (32 KB per wave
@@ -231,6 +233,7 @@ struct AttnTile {
     static constexpr int THREADS = 64 * NR * NK, BM = 16 * RT * NR, BN = BN_, KW = BN / NK, KB = KW / 16;
     static constexpr int NB = NB_;                               // buffered tiles
     static constexpr bool DMA = FMT == kKvBf16;                  // straight into LDS
+    static constexpr bool TWO = DMA && BM <= 64;                 // weights in two bf16 parts
     static constexpr int ROWB = D * 2;                           // bytes of a row in LDS
     static constexpr int ES = DMA ? 2 : 1, CPR = D * ES / 16;    // 16-byte chunks of a cache row
     static constexpr int NCH = BN * CPR / THREADS;               // chunks of K (and of V) per thread
@@ -258,7 +261,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 {
     using TL = AttnTile<D, FMT, NR, NK, RT, BN, NB>;
     constexpr int THREADS = TL::THREADS, BM = TL::BM, KW = TL::KW, KB = TL::KB, NCH = TL::NCH, CPR = TL::CPR;
-    constexpr bool DMA = TL::DMA;
+    constexpr bool DMA = TL::DMA, TWO = TL::TWO;
     using P8 = std::conditional_t<DMA, bf16x8_t, f16x8_t>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     int *bad = reinterpret_cast<int *>(lds + TL::o_bad);  // v of the item's tiles held something not finite
@@ -588,7 +591,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                             for (int i = 0; i < 4; ++i) o[rt][cb][i] *= f;
                     }
                 }
-                P8 pf[RT][KB / 2];
+                P8 pf[RT][KB / 2], pl[TWO ? RT : 1][TWO ? KB / 2 : 1];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
                     f4 iv = f4{1.f, 1.f, 1.f, 1.f};
@@ -604,6 +607,8 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                             else
                                 l[rt] = __builtin_fmaf(w, iv[i], l[rt]);
                             pf[rt][kb / 2][4 * (kb % 2) + i] = w;
+                            if constexpr (TWO)
+                                pl[rt][kb / 2][4 * (kb % 2) + i] = (__bf16)(w - (float)pf[rt][kb / 2][4 * (kb % 2) + i]);
                         }
                     }
                 }
@@ -616,7 +621,10 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                         const int c = ((2 * cb + ((li & 3) >> 1)) ^ z) * 16;
                         const P8 vf = __builtin_bit_cast(P8, u64x2_t{lds_tr4(base + c), lds_tr4(base + c + 16 * TL::ROWB)});
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) o[rt][cb] = mfma_vp(vf, pf[rt][kp], o[rt][cb]);
+                        for (int rt = 0; rt < RT; ++rt) {
+                            o[rt][cb] = mfma_vp(vf, pf[rt][kp], o[rt][cb]);
+                            if constexpr (TWO) o[rt][cb] = mfma_vp(vf, pl[rt][kp], o[rt][cb]);
+                        }
                     }
                 }
             };
