@@ -29,8 +29,7 @@
 // folded into the exponent, w_j = 2^(s_j + log2 vs_j - m) with m the maximum of that sum (or up to 8 below it),
 // so no weight passes 2^8 whatever the scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's
 // own sum takes w_j / vs_j in fp32.  (That holds while the v scales of the keys a workgroup meets lie within
-// 2^100 of each other; one below 2^-64 counts as that, which moves an output by at most 448 2^-64, and 0, which
-// goes with codes of 0, as 1.)
+// 2^100 of each other.  One below 2^-64, 0 among them, counts as 2^-64, which moves an output by at most 448 2^-64.)
 //
 // What bounds it.  Few rows per key: the cache's bytes (64 tokens over 50 .. 20000 keys each, 8 heads, e4m3:
 // 1.35 GB in 245 us, 5.5 TB/s, as fast as a large copy).  Many rows per key: a tile's LDS reads (32 KB per wave
@@ -447,8 +446,9 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                             sreg = 0.0f;
                             *bad = 1;
                         }
-                        // 2^-64 at least: 1 / vs and the sums of w / vs stay finite (a NaN stays one)
-                        const float vs = sreg == 0.0f ? 1.0f : sreg < 0x1p-64f ? 0x1p-64f : sreg;
+                        // 2^-64 at least: 1 / vs and the sums of w / vs stay finite (a NaN stays one), and a row of
+                        // zeros (scale 0) adds its weight to the sum without lifting the maximum of s + log2 vs
+                        const float vs = sreg < 0x1p-64f ? 0x1p-64f : sreg;
                         sc[BN + srow] = __builtin_amdgcn_logf(vs);  // base 2
                         sc[2 * BN + srow] = 1.0f / vs;
                     }

@@ -556,8 +556,8 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  * Scores, maxima and sums are in fp32; for the product with v the weights are rounded to fp16 (8 bits),
  * or (bf16 cache) to bf16, in two parts, hi and lo, where at most 64 rows share their keys.  A key that a row does not see does not reach it, whatever its k and v
  * hold.  A row whose keys are all on pages outside the pool is zero.  Scales of an 8-bit cache are not
- * negative; a v scale of 0 goes with codes of 0, one below 2^-64 counts as 2^-64, and those of the
- * keys of a call lie within 2^100 of each other.
+ * negative; a v scale below 2^-64, 0 among them, counts as 2^-64, and counted so those of the keys of a
+ * call lie within 2^100 of each other.
  *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
  *   gdn_kv_write; out may be q itself.  scale: > 0, scale log2(e) finite in fp32.
  *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
