@@ -26,9 +26,11 @@
 // beyond, where the second part's products would cost 5 .. 22% (128 and 256 rows) for an error of 2^-9 of a
 // weight, rms, beside the 2^-9 of the stored result.  8-bit codes travel through registers and are widened on
 // the way into LDS, k to bf16 and v to fp16, both exactly.  The k scale multiplies the scores; the v scale is
-// folded into the exponent, w_j = 2^(s_j + log2 vs_j - m) with m the maximum of that sum (or up to 8 below it),
-// so no weight passes 2^8 whatever the scales are and rounding to fp16 costs 2^-12 of a weight; the softmax's
-// own sum takes w_j / vs_j in fp32.  (That holds while the v scales of the keys a workgroup meets lie within
+// folded into the exponent, w_j = 2^(s_j + log2 vs_j - m) with m 7 to 15 below the maximum of that sum, so the
+// largest weight lies in 2^7 .. 2^15 whatever the scales are and rounding to fp16 costs at most 2^-11 of a weight
+// down to 2^-21 of the largest, and 2^-32 of the largest below that (where one key draws nearly all of a row, the
+// others are that small, and they alone make the channels in which its v is 0); the softmax's own sum takes
+// w_j / vs_j in fp32.  (That holds while the v scales of the keys a workgroup meets lie within
 // 2^100 of each other.  One below 2^-64, 0 among them, counts as 2^-64, which moves an output by at most 448 2^-64.)
 //
 // What bounds it.  Few rows per key: the cache's bytes (64 tokens over 50 .. 20000 keys each, 8 heads, e4m3:
@@ -51,7 +53,8 @@ typedef unsigned long long u64x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kSlack = 8.0f;  // weights reach 2^8 where fp16 ends at 2^16
+constexpr float kSlack = 8.0f;  // how far the maximum may grow before the sums are rescaled
+constexpr float kLift = 7.0f;   // 8-bit caches: the largest weight starts at 2^7 and reaches 2^15 where fp16 ends at 2^16
 
 __device__ __forceinline__ f4 mfma_kq(bf16x8_t a, bf16x8_t b, f4 c)
 {
@@ -261,6 +264,7 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
     using TL = AttnTile<D, FMT, NR, NK, RT, BN, NB>;
     constexpr int THREADS = TL::THREADS, BM = TL::BM, KW = TL::KW, KB = TL::KB, NCH = TL::NCH, CPR = TL::CPR;
     constexpr bool DMA = TL::DMA, TWO = TL::TWO;
+    constexpr float LIFT = DMA ? 0.0f : kLift;  // bf16 weights have fp32's range
     using P8 = std::conditional_t<DMA, bf16x8_t, f16x8_t>;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     int *bad = reinterpret_cast<int *>(lds + TL::o_bad);  // v of the item's tiles held something not finite
@@ -577,12 +581,12 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     if constexpr (DMA) top[rt] *= a.scale;
-                    grew |= top[rt] - m[rt] > kSlack;  // from -inf as well
+                    grew |= top[rt] - m[rt] > kSlack + LIFT;  // from -inf as well
                 }
                 if (__any(grew)) {
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
-                        const float mn = fmaxf(m[rt], quad_max(top[rt])), f = exp2_f(m[rt] - finite_max(mn));
+                        const float mn = fmaxf(m[rt], quad_max(top[rt]) - LIFT), f = exp2_f(m[rt] - finite_max(mn));
                         m[rt] = mn;
                         l[rt] *= f;
 #pragma unroll

@@ -553,9 +553,10 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  * pages prefix_pages (device int32 [max_prefix_pages]): a prefix that all share, held once, and
  * scored for the rows of all entries together, so its pages are read once for the batch.
  *   out = sum_j softmax_j(scale q . k_j) v_j,  query head h reading KV head h / (n_q / n_kv).
- * Scores, maxima and sums are in fp32; for the product with v the weights are rounded to fp16 (8 bits),
- * or (bf16 cache) to bf16, in two parts, hi and lo, where at most 64 rows share their keys.  A key that a row does not see does not reach it, whatever its k and v
- * hold.  A row whose keys are all on pages outside the pool is zero.  Scales of an 8-bit cache are not
+ * Scores, maxima and sums are in fp32; for the product with v the weights are rounded to fp16 (8 bits:
+ * 2^-11 of a weight times v scale down to 2^-21 of the row's largest, then 2^-32 of the largest), or (bf16
+ * cache) to bf16, in two parts, hi and lo, where at most 64 rows share their keys.  A key that a row does
+ * not see does not reach it, whatever its k and v hold.  A row whose keys are all on pages outside the pool is zero.  Scales of an 8-bit cache are not
  * negative; a v scale below 2^-64, 0 among them, counts as 2^-64, and counted so those of the keys of a
  * call lie within 2^100 of each other.
  *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
