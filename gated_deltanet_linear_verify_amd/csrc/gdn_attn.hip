@@ -633,8 +633,11 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                 }
             };
 
-            if (tid == 0) *bad = 0;  // before the loop's first barrier
+            // A barrier lies between this and the first store of 1: with one buffer or a bf16 cache the loop's
+            // first one, else the one here, under which the first tile's loads are on their way.
+            if (tid == 0) *bad = 0;
             issue(kt0, 0);
+            if constexpr (!DMA && NB > 1) __syncthreads();
 #pragma unroll 1
             for (int kt = kt0; kt < kt1; ++kt) {
                 const int buf = NB > 1 ? (kt - kt0) & 1 : 0;

@@ -1,6 +1,7 @@
 """Attention over the paged cache where single keys differ from the rest: a key that draws most of the attention
-and has nothing in v, or nothing but one channel.  Held to the definition in 64 bits, with the bound of the attention
-tests or with the one below that takes each cache format for what its weights are rounded to."""
+and has nothing in v, or nothing but one channel; values that are not finite.  Held to the definition in 64 bits,
+with the bound of the attention tests or with the one below that takes each cache format for what its weights are
+rounded to."""
 
 import numpy as np
 import pytest
@@ -132,3 +133,28 @@ def test_a_strong_key_with_one_channel(rows, fmt, d):
         codes[pg, :, at, 1:] = 0
     c.upload()
     say(f"{rows}, {fmt}, d {d}: {c.check(c.run()):.2f} of the bound")
+
+
+@pytest.mark.parametrize("grp,T", [(2, 8), (4, 16), (4, 20), (8, 32)])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_values_that_are_not_finite_in_every_first_tile(fmt, grp, T):
+    """Entries whose only tile holds drafted keys, one of them with a v that is not finite: every entry's rows that see
+    it have it in their result, in every one of several runs (16, 64, 80 and 256 rows share keys)."""
+    n = 48
+    c = Case(fmt, 128, 2, grp, 64, [(7 * i) % 20 for i in range(n)], T, seed=T)
+    for b in range(n):
+        pos = int(c.ctx[b]) + b % T
+        pg, at = int(c.table[b][pos // 64]), pos % 64
+        if fmt == "bf16":
+            c.store["v"][pg, b % 2, at, 7 * b % 128] = float("inf") if b % 3 else float("nan")
+        elif fmt == "e4m3" and b % 3:
+            c.store["v"].view(torch.uint8)[pg, b % 2, at, 7 * b % 128] = 0x7f
+        else:
+            c.store["v_scale"][pg, b % 2, at] = float("nan")
+    c.upload()
+    with np.errstate(all="ignore"):
+        c.check(c.run())
+    first = torch.nan_to_num(c.out.float(), nan=-5.0)
+    for _ in range(5):
+        again = c.run(out=torch.full_like(c.out, 7.0))
+        assert torch.equal(torch.nan_to_num(again.float(), nan=-5.0), first)
