@@ -21,7 +21,7 @@
 // on both operands).
 //
 // Formats.  A bf16 cache goes into LDS as it is (global_load_lds), and the second product takes its
-// weights in bf16: in two parts (2^-17 of a weight is lost) in tiles of up to 64 rows, which the cache's
+// weights in bf16: in two parts (at most 2^-15 of a weight is lost) in tiles of up to 64 rows, which the cache's
 // bytes bound (32 entries of 1000 .. 4000 keys, 16 to 64 rows: d 128 + 0 .. 1%, d 256 + 2 .. 4%), in one
 // beyond, where the second part's products would cost 5 .. 22% (128 and 256 rows) for an error of 2^-9 of a
 // weight, rms, beside the 2^-9 of the stored result.  8-bit codes travel through registers and are widened on
@@ -101,6 +101,13 @@ __device__ __forceinline__ float quad_sum(float x)
 // 2^(x - m) with 2^(-inf - -inf) = 0: m is the finite stand-in of soft_max below.
 __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float finite_max(float m) { return m == kNegInf ? 0.0f : m; }
+
+// The bf16 value next below w > 0 (below, where w is one itself); 0 for 0, a NaN for a NaN.  What is left of w is
+// positive, so an infinity of v times either part keeps its sign (a rest of 0 or less would make it a NaN).
+__device__ __forceinline__ float bf16_below(float w)
+{
+    return __uint_as_float(__builtin_elementwise_sub_sat(__float_as_uint(w), 1u) & 0xffff0000u);
+}
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -610,9 +617,13 @@ __global__ __launch_bounds__(64 * NR * NK, (AttnTile<D, FMT, NR, NK, RT, BN, NB>
                                 l[rt] += w;
                             else
                                 l[rt] = __builtin_fmaf(w, iv[i], l[rt]);
-                            pf[rt][kb / 2][4 * (kb % 2) + i] = w;
-                            if constexpr (TWO)
-                                pl[rt][kb / 2][4 * (kb % 2) + i] = (__bf16)(w - (float)pf[rt][kb / 2][4 * (kb % 2) + i]);
+                            if constexpr (TWO) {
+                                const float hi = bf16_below(w);
+                                pf[rt][kb / 2][4 * (kb % 2) + i] = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(hi) >> 16));
+                                pl[rt][kb / 2][4 * (kb % 2) + i] = (__bf16)(w - hi);
+                            } else {
+                                pf[rt][kb / 2][4 * (kb % 2) + i] = w;
+                            }
                         }
                     }
                 }

@@ -158,3 +158,22 @@ def test_values_that_are_not_finite_in_every_first_tile(fmt, grp, T):
     for _ in range(5):
         again = c.run(out=torch.full_like(c.out, 7.0))
         assert torch.equal(torch.nan_to_num(again.float(), nan=-5.0), first)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("grp,T,prefix", [(1, 1, 0), (4, 8, 0), (4, 16, 0), (8, 16, 0), (8, 32, 0), (2, 2, 300), (8, 24, 300)])
+def test_values_that_are_not_finite_in_the_context(grp, T, prefix, fmt, d):
+    """Infinities and a NaN in v of cached keys that every row sees, in a prefix too: each in its channel, with its
+    sign, however the weights are split for the product."""
+    c = Case(fmt, d, 1, grp, 16, [200, 90], T, prefix=prefix, seed=3)
+    for pages in ([c.shared] if prefix else []) + [c.table[0]]:
+        for pos, ch, x in ((5, 3, float("inf")), (70, 9, float("-inf")), (71, 11, float("nan"))):
+            pg, at = int(pages[pos // 16]), pos % 16
+            if fmt == "bf16":
+                c.store["v"][pg, 0, at, ch] = x
+            else:  # NaN is all that e4m3 has
+                c.store["v"].view(torch.uint8)[pg, 0, at, ch] = 0x7f
+    c.upload()
+    with np.errstate(all="ignore"):
+        say(f"{c.check(c.run()):.2f} of the bound")
