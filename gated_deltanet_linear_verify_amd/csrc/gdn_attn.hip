@@ -1007,7 +1007,7 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
                    : tile_sizes_f<256>(format, ph.cfg, ph.bn, per_cu);
         const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
         const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
-        if (rows * entries > kMaxTokenRows || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
+        if (rows * entries >= kMaxTokenRows || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
             (double)items * n_kv * (double)tiles >= 2147483648.0) {
             fits = false;
             return;
@@ -1068,7 +1068,6 @@ static hipError_t launch_attn_d(const AttnArgs &a, hipStream_t stream)
                : a.kv.format == kKvE4m3 ? launch_cfg<D, kKvE4m3, P>(a, stream)
                                         : launch_cfg<D, kKvI8, P>(a, stream);
     };
-    const int64_t rows = (int64_t)a.b.n_batch * a.b.n_tok;
     if (a.parent) {
         hipLaunchKernelGGL(attn_ancestors_kernel, dim3((unsigned)a.b.n_batch), dim3(256), 0, stream, a);
         if (hipError_t e = hipGetLastError()) return e;

@@ -65,7 +65,7 @@ GDN_API size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n
     }
     gdn::AttnPlan p;
     if (!gdn::attn_plan(kv->d, kv->format, kv->page_size, kv->n_kv, n_q / kv->n_kv, n_batch, n_tok, 1, prefix != 0, 1, p)) {
-        abi_fail(GDN_ERR_SHAPE, "%s: too many rows", fn);
+        abi_fail(GDN_ERR_SHAPE, "%s: 2^26 rows of a KV head or more", fn);
         return 0;
     }
     return p.bytes;

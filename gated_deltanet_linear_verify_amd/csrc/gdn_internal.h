@@ -178,8 +178,8 @@ struct KvCommitArgs {
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t stream);
 // Attention of drafted tokens (gdn_attn.hip).  A launch's work is a list of items, each a tile of query
 // rows of one KV head with the keys they see; AttnPhase describes one launch's items.
-// Token rows of a call (for attention: times the query heads of a group): 2^26 rows of 32 lanes, or the
-// join's of 64, stay below the 2^32 threads of a launch's x axis.
+// Token rows of a call: 2^26 rows of 32 lanes stay below the 2^32 threads of a launch's x axis.  For attention,
+// token rows times the query heads of a group: fewer than 2^26, as the join takes 64 lanes for each.
 constexpr int64_t kMaxTokenRows = (int64_t)1 << 26;
 
 struct AttnPhase {

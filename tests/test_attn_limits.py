@@ -1,0 +1,49 @@
+"""The ends of what the full-attention layers' entry points take, on the host: no launch is made."""
+
+import ctypes
+import os
+
+import pytest
+
+from gated_deltanet_linear_verify_amd import gdn
+
+FAKE = 0x1000  # aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(gdn.LIB_PATH):
+        pytest.skip("libgdn.so not built")
+    return gdn.lib()
+
+
+def _rows(n_heads=4, d=128, **kw):
+    return gdn.gdn_rows(**{**dict(ptr=FAKE, ld=n_heads * d, hd=d, n_heads=n_heads, dtype=gdn.GDN_BF16), **kw})
+
+
+def _kv(**kw):
+    return gdn.gdn_kv(**{**dict(n_kv=4, d=128, page_size=64, n_pages=10, format=gdn.GDN_KV_I8, flags=0, k=FAKE, v=FAKE,
+                                k_scale=FAKE, v_scale=FAKE), **kw})
+
+
+def _batch(**kw):
+    return gdn.gdn_kv_batch(**{**dict(block_table=FAKE, start=FAKE, n_new=None, max_pages=4, n_batch=2, n_tok=3), **kw})
+
+
+def _attn(L, kv=None, batch=None, q=None, out=None, pages=None, n_pages=0, plen=None, ws_bytes=1 << 62):
+    """gdn_attn_verify with a workspace that is too small unless ws_bytes says otherwise: the check that comes last."""
+    return L.gdn_attn_verify(ctypes.byref(kv or _kv()), ctypes.byref(batch or _batch()), None, pages, n_pages, plen,
+                             ctypes.byref(q or _rows()), ctypes.byref(out or _rows(ptr=2 * FAKE)), 0.1, FAKE, ws_bytes, None)
+
+
+def test_attention_rows_stay_below_what_a_launch_holds(L):
+    """2^26 rows of 64 lanes (d 256) would be 2^32 threads, one too many."""
+    kv = _kv(n_kv=1, d=256)
+    ws = lambda n_q, b, t, p: L.gdn_attn_workspace_bytes(ctypes.byref(kv), n_q, b, t, p)  # noqa: E731
+    for n_q, b, t in ((1, 1 << 13, 1 << 13), (4, 1 << 12, 1 << 12), (65536, 1 << 10, 1)):
+        for prefix in (0, 1):
+            assert ws(n_q, b, t, prefix) == 0 and "2^26" in gdn.last_error()
+            assert ws(n_q, b - 1, t, prefix) > 0
+        r, o = (_rows(n_heads=n_q, d=256, ptr=p) for p in (FAKE, 2 * FAKE))
+        assert _attn(L, kv, _batch(n_batch=b, n_tok=t), r, o) == gdn.GDN_ERR_SHAPE
+        assert _attn(L, kv, _batch(n_batch=b - 1, n_tok=t), r, o, ws_bytes=16) == gdn.GDN_ERR_ARG  # only the workspace
