@@ -1007,7 +1007,9 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
                    : tile_sizes_f<256>(format, ph.cfg, ph.bn, per_cu);
         const int64_t row_tiles = (rows + ph.bm - 1) / ph.bm, items = row_tiles * entries;
         const int64_t tiles = (pages * page_size + ph.bn - 1) / ph.bn;
-        if (rows * entries >= kMaxTokenRows || items * n_kv >= (int64_t)1 << 30 || pages * page_size >= (int64_t)1 << 31 ||
+        // The kernels count positions in 32 bits, up to a table's end and a call's tokens or a tile beyond it.
+        if (rows * entries >= kMaxTokenRows || items * n_kv >= (int64_t)1 << 30 ||
+            pages * page_size + std::max(n_tok, ph.bn) >= (int64_t)1 << 31 ||
             (double)items * n_kv * (double)tiles >= 2147483648.0) {
             fits = false;
             return;

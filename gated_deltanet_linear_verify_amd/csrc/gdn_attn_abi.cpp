@@ -94,7 +94,7 @@ GDN_API int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const i
     a.grp = q->n_heads / kv->n_kv;
     if (!gdn::attn_plan(kv->d, kv->format, kv->page_size, kv->n_kv, a.grp, batch->n_batch, batch->n_tok, batch->max_pages,
                         prefix_pages != nullptr, max_prefix_pages, a.plan))
-        return abi_fail(GDN_ERR_SHAPE, "%s: the call's tiles pass 2^31", fn);
+        return abi_fail(GDN_ERR_SHAPE, "%s: the call's tiles or its tables' positions pass 2^31", fn);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u))
         return abi_fail(GDN_ERR_ARG, "%s: workspace must be 16-byte aligned device memory", fn);
     if (ws_bytes < a.plan.bytes)

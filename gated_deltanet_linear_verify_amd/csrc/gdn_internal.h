@@ -207,7 +207,7 @@ struct AttnArgs {
     unsigned char *ws;
     AttnPlan plan;
 };
-// Sizes only; false where a launch's tiles would pass 2^31.
+// Sizes only; false where a launch's rows, tiles or positions would pass what the kernels count in.
 bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch, int n_tok, int max_pages, bool prefix,
                int max_prefix_pages, AttnPlan &p);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);

@@ -564,7 +564,8 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
  *   calls (and recorded graphs) that may run at the same time need one each.
  * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, or a bad scale ->
- * GDN_ERR_ARG; sizes whose key tiles would pass 2^31, or n_batch n_tok n_q / n_kv >= 2^26 -> GDN_ERR_SHAPE.
+ * GDN_ERR_ARG; sizes whose key tiles would pass 2^31, a table or prefix of 2^31 - max(n_tok, 64) positions or
+ * more, or n_batch n_tok n_q / n_kv >= 2^26 -> GDN_ERR_SHAPE.
  */
 int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *parent,
                     const int32_t *prefix_pages, int32_t max_prefix_pages, const int32_t *prefix_len,

@@ -47,3 +47,13 @@ def test_attention_rows_stay_below_what_a_launch_holds(L):
         r, o = (_rows(n_heads=n_q, d=256, ptr=p) for p in (FAKE, 2 * FAKE))
         assert _attn(L, kv, _batch(n_batch=b, n_tok=t), r, o) == gdn.GDN_ERR_SHAPE
         assert _attn(L, kv, _batch(n_batch=b - 1, n_tok=t), r, o, ws_bytes=16) == gdn.GDN_ERR_ARG  # only the workspace
+
+
+def test_attention_positions_stay_in_32_bits(L):
+    """A table's end plus the call's tokens, and the tile that holds it, have to be int32 positions."""
+    for page, n_tok in ((16, 3), (64, 1), (4096, 5000), (64, 1000)):
+        most = ((1 << 31) - max(n_tok, 64) - 1) // page  # pages
+        kv, r = _kv(page_size=page, n_kv=1), _rows(n_heads=1)
+        for pages, code in ((most, gdn.GDN_ERR_ARG), (most + 1, gdn.GDN_ERR_SHAPE)):  # ARG: the workspace, looked at last
+            assert _attn(L, kv, _batch(n_batch=1, n_tok=n_tok, max_pages=pages), r, r, ws_bytes=16) == code, (page, n_tok, pages)
+            assert _attn(L, kv, _batch(n_batch=1, n_tok=n_tok), r, r, pages=FAKE, n_pages=pages, plen=FAKE, ws_bytes=16) == code
