@@ -84,6 +84,10 @@ GDN_API int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const i
     if (int r = gdn::abi_check_rows(fn, "out", out, q->n_heads)) return r;
     if (int r = gdn::abi_check_apart(fn, "out", out, (int64_t)batch->n_batch * batch->n_tok, kv->d)) return r;
     if (q->dtype != GDN_BF16 || out->dtype != GDN_BF16) return abi_fail(GDN_ERR_DTYPE, "%s: q and out must be GDN_BF16", fn);
+    // Workgroups read rows of q that others have not reached yet: out may only lie where the same row of q does.
+    const int64_t rows = (int64_t)batch->n_batch * batch->n_tok;
+    if (q->ptr == out->ptr && ((rows > 1 && q->ld != out->ld) || (q->n_heads > 1 && q->hd != out->hd)))
+        return abi_fail(GDN_ERR_ARG, "%s: out is q's memory with other strides", fn);
     if (!(scale > 0.0f) || !std::isfinite(scale * gdn::kLog2E)) return abi_fail(GDN_ERR_ARG, "%s: scale must be finite and > 0", fn);
     if (parent && batch->n_tok > kMaxTreeNodes)
         return abi_fail(GDN_ERR_SHAPE, "%s: a tree of %d nodes, at most %d", fn, batch->n_tok, kMaxTreeNodes);

@@ -560,11 +560,11 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  * negative; a v scale below 2^-64, 0 among them, counts as 2^-64, and counted so those of the keys of a
  * call lie within 2^100 of each other.
  *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
- *   gdn_kv_write; out may be q itself.  scale: > 0, scale log2(e) finite in fp32.
+ *   gdn_kv_write; out may be q itself, with the same strides, otherwise they must not overlap.  scale: > 0, scale log2(e) finite in fp32.
  *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
  *   calls (and recorded graphs) that may run at the same time need one each.
- * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, or a bad scale ->
- * GDN_ERR_ARG; sizes whose key tiles would pass 2^31, a table or prefix of 2^31 - max(n_tok, 64) positions or
+ * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, a bad scale, or out on
+ * q's memory with other strides -> GDN_ERR_ARG; sizes whose key tiles would pass 2^31, a table or prefix of 2^31 - max(n_tok, 64) positions or
  * more, or n_batch n_tok n_q / n_kv >= 2^26 -> GDN_ERR_SHAPE.
  */
 int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *parent,

@@ -57,3 +57,16 @@ def test_attention_positions_stay_in_32_bits(L):
         for pages, code in ((most, gdn.GDN_ERR_ARG), (most + 1, gdn.GDN_ERR_SHAPE)):  # ARG: the workspace, looked at last
             assert _attn(L, kv, _batch(n_batch=1, n_tok=n_tok, max_pages=pages), r, r, ws_bytes=16) == code, (page, n_tok, pages)
             assert _attn(L, kv, _batch(n_batch=1, n_tok=n_tok), r, r, pages=FAKE, n_pages=pages, plen=FAKE, ws_bytes=16) == code
+
+
+def test_attention_in_place_takes_the_same_strides(L):
+    """out on q's memory: the same rows at the same places, or a row that one workgroup writes is another's q."""
+    def code(rows, q, out):
+        return _attn(L, batch=_batch(n_batch=1, n_tok=rows), q=_rows(**q), out=_rows(**out), ws_bytes=16)
+    same, wide, turned = dict(ptr=FAKE), dict(ptr=FAKE, ld=1024), dict(ptr=FAKE, ld=128, hd=384)
+    small = "workspace smaller"  # what is looked at last
+    assert code(3, same, same) == gdn.GDN_ERR_ARG and small in gdn.last_error()
+    assert code(3, same, dict(ptr=2 * FAKE, ld=1024)) == gdn.GDN_ERR_ARG and small in gdn.last_error()
+    for rows, q, out in ((3, same, wide), (3, wide, same), (3, same, turned), (1, same, turned)):
+        assert code(rows, q, out) == gdn.GDN_ERR_ARG and "strides" in gdn.last_error()
+    assert code(1, same, wide) == gdn.GDN_ERR_ARG and small in gdn.last_error()  # one row: nothing is stepped over
