@@ -100,9 +100,26 @@ int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_he
     return GDN_OK;
 }
 
+// Runs of d elements at a ld + b hd, 0 <= a < n_rows, 0 <= b < n_heads, apart from each other?  Two of them overlap
+// where |a ld + b hd| < d for differences a, b that are not both 0.
+static bool rows_apart(const gdn_rows *r, int64_t n_rows, int d)
+{
+    __int128 ld = r->ld, hd = r->hd;
+    if (ld < 0) ld = -ld;
+    if (hd < 0) hd = -hd;  // the mirrored case has the same differences, with the other sign of a
+    const __int128 a_max = n_rows - 1, b_max = r->n_heads - 1;
+    if ((a_max > 0 && ld < d) || (b_max > 0 && hd < d)) return false;
+    if (a_max == 0 || b_max == 0 || ld >= b_max * hd + d || hd >= a_max * ld + d) return true;  // one inside the other
+    for (__int128 b = 1; b <= b_max; ++b) {
+        const __int128 a = b * hd / ld;  // the difference in rows that comes nearest from below, and the next one
+        if ((a <= a_max && b * hd - a * ld < d) || (a < a_max && (a + 1) * ld - b * hd < d)) return false;
+    }
+    return true;
+}
+
 int abi_check_apart(const char *fn, const char *what, const gdn_rows *r, int64_t n_rows, int d)
 {
-    if ((n_rows > 1 && r->ld > -d && r->ld < d) || (r->n_heads > 1 && r->hd > -d && r->hd < d))
+    if (!rows_apart(r, n_rows, d))
         return abi_fail(GDN_ERR_ARG, "%s: %s: rows or heads that are written lie on top of each other", fn, what);
     return GDN_OK;
 }

@@ -403,7 +403,7 @@ int gdn_linear(const void *x, const void *w, int32_t M, int32_t N, int32_t K, co
  * gdn_rows names per-token rows of heads: the d channels of head h of token t start at
  * ptr + (t * ld + h * hd) elements, contiguous; ld and hd may be any strides, so q, k and v may
  * stay inside the fused rows that one projection wrote.  Rows that are read may repeat (a stride of
- * 0); rows that are written must not overlap, and strides of less than d there are GDN_ERR_ARG.
+ * 0); rows that are written must not overlap: strides that put one on another are GDN_ERR_ARG.
  */
 typedef struct gdn_rows {
     void *ptr;

@@ -3,6 +3,7 @@
 import ctypes
 import os
 
+import numpy as np
 import pytest
 
 from gated_deltanet_linear_verify_amd import gdn
@@ -70,3 +71,27 @@ def test_attention_in_place_takes_the_same_strides(L):
     for rows, q, out in ((3, same, wide), (3, wide, same), (3, same, turned), (1, same, turned)):
         assert code(rows, q, out) == gdn.GDN_ERR_ARG and "strides" in gdn.last_error()
     assert code(1, same, wide) == gdn.GDN_ERR_ARG and small in gdn.last_error()  # one row: nothing is stepped over
+
+
+def test_written_rows_on_top_of_each_other_are_refused(L):
+    """Every combination of strides, against a count of the elements that two rows share."""
+    table = gdn.gdn_rope_init(2)
+    d, rng = 8, np.random.default_rng(0)
+    cases = [(3, 4, 8, 8), (3, 4, 32, 8), (3, 4, 8, 24), (3, 4, 8, 16), (2, 2, 16, 24), (5, 3, 24, 16), (5, 3, 24, -16), (1, 4, 0, 8),
+             (4, 1, 8, 0), (2, 3, -40, 12), (2, 3, 9, 1 << 62), (70000, 5, 1 << 40, 1 << 20)]
+    cases += [tuple(int(x) for x in (*rng.integers(1, 7, 2), *rng.integers(-60, 61, 2))) for _ in range(3000)]
+    seen = {True: 0, False: 0}
+    for n, heads, ld, hd in cases:
+        if n * heads < 1000:
+            starts = sorted(a * ld + b * hd for a in range(n) for b in range(heads))
+            apart = all(b - a >= d for a, b in zip(starts, starts[1:]))
+        else:
+            apart = True
+        x = gdn.gdn_rows(FAKE, 0, 0, heads, gdn.GDN_F32)
+        out = gdn.gdn_rows(2 * FAKE, ld, hd, heads, gdn.GDN_F32)
+        # the segment behind it has a NULL pointer: the check that comes after the first one's
+        xs, outs = (gdn.gdn_rows * 2)(x, gdn.gdn_rows()), (gdn.gdn_rows * 2)(out, gdn.gdn_rows())
+        assert L.gdn_rope(ctypes.byref(table), xs, outs, 2, d, FAKE, n, 0, None) == gdn.GDN_ERR_ARG
+        assert ("NULL" if apart else "on top of") in gdn.last_error(), (n, heads, ld, hd)
+        seen[apart] += 1
+    assert min(seen.values()) > 500
