@@ -343,16 +343,19 @@ GDN_API int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int
     if (int r = gdn::abi_check_places(fn, kv, batch, false, st)) return r;
     if (kv->flags & GDN_F_CHECK_INDICES) {
         const size_t B = batch->n_batch, n = B * max_path;
-        std::unique_ptr<int32_t[]> h(new (std::nothrow) int32_t[n + B]);
+        std::unique_ptr<int32_t[]> h(new (std::nothrow) int32_t[n + 2 * B]);
         if (!h) return abi_fail(GDN_ERR_HIP, "%s: no host memory for the index check", fn);
         if (int r = gdn::abi_fetch_i32(path, n, st, h.get())) return r;
         if (int r = gdn::abi_fetch_i32(n_path, B, st, h.get() + n)) return r;
+        if (batch->n_new) {
+            if (int r = gdn::abi_fetch_i32(batch->n_new, B, st, h.get() + n + B)) return r;
+        }
         for (size_t b = 0; b < B; ++b) {
-            const int32_t m = h[n + b];
+            const int32_t m = h[n + b], nodes = batch->n_new ? h[n + B + b] : batch->n_tok;
             if (m < 0 || m > max_path) return abi_fail(GDN_ERR_RANGE, "%s: n_path[%zu] = %d outside [0, max_path]", fn, b, m);
             for (int32_t j = 0; j < m; ++j) {
                 const int32_t node = h[b * max_path + j];
-                if (node < (j ? h[b * max_path + j - 1] + 1 : 0) || node >= batch->n_tok)
+                if (node < (j ? h[b * max_path + j - 1] + 1 : 0) || node >= nodes)
                     return abi_fail(GDN_ERR_RANGE, "%s: path[%zu][%d] = %d is no increasing node index", fn, b, j, node);
             }
         }

@@ -536,8 +536,8 @@ int gdn_kv_read(const gdn_kv *kv, const gdn_kv_batch *batch, const gdn_rows *k, 
  * Keep the accepted path of a verified tree (what gdn_rollback does for the GDN layers): for each
  * entry the cache rows of nodes path[b][0 .. n_path[b]) (device int32 [n_batch][max_path], strictly
  * increasing node indices) move to positions start[b], start[b] + 1, ...; codes and scales are
- * copied bit for bit.  n_path[b] is taken as at most max_path.  batch->n_tok is the tree's node count;
- * a path entry that is not a node index, or is below its own place in the path, is skipped.  As in
+ * copied bit for bit.  n_path[b] is taken as at most max_path.  batch->n_tok is the tree's node count
+ * (n_new[b], where given, that of entry b's); a path entry that is not a node index, or is below its own place in the path, is skipped.  As in
  * gdn_kv_write, two entries must not have the same places there.
  */
 int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *path,

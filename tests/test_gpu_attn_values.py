@@ -177,3 +177,24 @@ def test_values_that_are_not_finite_in_the_context(grp, T, prefix, fmt, d):
     c.upload()
     with np.errstate(all="ignore"):
         say(f"{c.check(c.run()):.2f} of the bound")
+
+
+def test_index_check_refuses_paths_of_nodes_that_do_not_count():
+    """gdn_kv_commit moves no row of a token at or past n_new; under GDN_F_CHECK_INDICES a path that names one is refused."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, v = (torch.randint(-127, 128, (4, 1, 16, 64), dtype=torch.int8, device="cuda") for _ in range(2))
+    kv = gdn.KvCache(k, v, *(torch.ones(4, 1, 16, device="cuda") for _ in range(2)))
+    kv.c.flags = gdn.GDN_F_CHECK_INDICES
+    table, start, path, before = i32([[0, 1], [2, 3]]), i32([10, 3]), i32([[1, 4], [0, 2]]), k.clone()
+    def commit(n_new):
+        gdn.gdn_kv_commit(kv, table, start, path, i32([2, 2]), 2, 6, n_new=None if n_new is None else i32(n_new))
+    for n_new in ([4, 6], [6, 2], [5, 0]):
+        with pytest.raises(gdn.GdnError) as e:
+            commit(n_new)
+        assert e.value.code == gdn.GDN_ERR_RANGE and torch.equal(k, before)
+    commit([5, 3])
+    assert torch.equal(k[0, 0, 10], before[0, 0, 11]) and torch.equal(k[0, 0, 11], before[0, 0, 14])
+    assert torch.equal(k[2, 0, 4], before[2, 0, 5])
+    k.copy_(before)
+    commit(None)
+    assert not torch.equal(k, before)
