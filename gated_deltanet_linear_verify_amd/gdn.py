@@ -388,7 +388,10 @@ def gdn_rope_init(rot_dim: int, *, theta: float = 1e4, layout: int = GDN_ROPE_HA
                   factor: float = 1.0, orig_ctx: int = 0, sections=None, beta_fast: float = 0.0,
                   beta_slow: float = 0.0, mscale: float = 0.0) -> gdn_rope_table:
     """The rotary table of the parameters (host memory, kept by the caller)."""
-    sec = (ctypes.c_int32 * 4)(*(list(sections) + [0, 0, 0, 0])[:4]) if sections else (ctypes.c_int32 * 4)()
+    sections = list(sections or ())
+    if len(sections) > 4:
+        raise GdnError(GDN_ERR_SHAPE, f"gdn_rope_init: {len(sections)} sections, at most 4 position axes")
+    sec = (ctypes.c_int32 * 4)(*sections)
     p = gdn_rope_params(rot_dim, layout, scaling, orig_ctx, sec, theta, factor, beta_fast, beta_slow, mscale)
     t = gdn_rope_table()
     _check(lib().gdn_rope_init(ctypes.byref(p), ctypes.byref(t)))

@@ -95,3 +95,12 @@ def test_written_rows_on_top_of_each_other_are_refused(L):
         assert ("NULL" if apart else "on top of") in gdn.last_error(), (n, heads, ld, hd)
         seen[apart] += 1
     assert min(seen.values()) > 500
+
+
+def test_rope_sections_are_all_counted(L):
+    """A fifth section is refused, whatever the first four add up to; fewer than four are followed by zeros."""
+    for sections in ((8, 8, 8, 8, 1), (32, 0, 0, 0, 0), (8, 8, 8, 4, 4)):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_rope_init(64, sections=sections)
+        assert e.value.code == gdn.GDN_ERR_SHAPE
+    assert list(gdn.gdn_rope_init(64, sections=(20, 12)).axis_end) == [20, 32, 32, 32]
