@@ -37,10 +37,12 @@
 // 1.35 GB in 245 us, 5.5 TB/s, as fast as a large copy).  Many rows per key: a tile's LDS reads (32 KB per wave
 // and tile), its softmax (240 vector instructions beside 64 MFMA at d 128 and 32 rows per wave) and its MFMA
 // follow one another in a wave, and two waves per SIMD, which is what the registers hold, overlap them only in
-// part: 8.1k shared keys under 64 x 16 rows (half of them there) of 32 heads in e4m3, 72 GFLOP, 115 us, 0.63
-// PFLOP/s of 1.40; the vector unit issues in 50% of the time, the matrix unit is busy in 37%.  A wave of 32 rows
-// at d <= 128 reads half the LDS bytes per row of one of 16 (the same call: 174 -> 164 us).  One token: latency
-// (11 us), a chain of three dependent loads (lengths, page, rows) and the joins between the key waves.
+// part: 8.1k shared keys under 64 x 16 rows (half of them there) of 32 heads in e4m3, 72 GFLOP, 120 us under the
+// profiler, 0.60 PFLOP/s of 1.40; the vector unit issues in 50% of the time, the matrix unit is busy in 37%.  A wave
+// of 32 rows at d <= 128 reads half the LDS bytes per row of one of 16 (the same call: 174 -> 164 us).  One token:
+// latency (11 us): a chain of three dependent loads (lengths, page, rows), two barriers of the scan before it, and the
+// joins between the key waves.  A long chain (8191 tokens at start 0): 1.2 ms, 0.46 PFLOP/s; from the first drafted
+// key on every tile is taken as one that some row may not see, though only the last of a row tile's are.
 #include <algorithm>
 #include <type_traits>
 

@@ -178,7 +178,7 @@ def block_step(d: dict, stream=None) -> None:
 
 def upload_attention(inp: dict, rope: "gdn.gdn_rope_table", *, fmt: int, page_size: int, n_pages: int,
                      prefix: bool = False) -> dict:
-    """Device tensors of one full-attention layer (workloads.make_attention_inputs): x [B*T][hidden], the
+    """Device tensors of one attention_step (workloads.make_attention_inputs): x [B*T][hidden], the
     concatenated weight w_in [(n_q + 2 n_kv) d][hidden], the fused rows qkv [B*T][n_q + 2 n_kv][d] with the
     views q, k and v of them, w_out, y, an empty cache of n_pages pages and the workspace.  The round's lists
     (start, positions, parent, n_new, prefix_pages, prefix_len) are the caller's, as device tensors."""
@@ -202,8 +202,10 @@ def upload_attention(inp: dict, rope: "gdn.gdn_rope_table", *, fmt: int, page_si
 
 def attention_step(d: dict, table, start, positions, n_new=None, parent=None, prefix_pages=None, prefix_len=None,
                    stream=None) -> None:
-    """One full-attention layer over every drafted token: the q, k and v projections as one gdn_linear, q rotated in
-    place, k rotated on its way into the cache, gdn_attn_verify of the chain or tree, the output projection."""
+    """The attention of a layer without norms of q and k, over every drafted token: the q, k and v projections as one
+    gdn_linear, q rotated in place, k rotated on its way into the cache, gdn_attn_verify of the chain or tree, the
+    output projection.  A layer that normalises the heads of q and k (lucebox-hub internal.h, struct TargetWeights:
+    q_norm, k_norm) makes these calls itself, with its norms of the views d["q"] and d["k"] behind the first."""
     B, T, kv, M = d["B"], d["T"], d["kv"], d["B"] * d["T"]
     N, Z = d["w_in"].shape[0], d["w_out"].shape[1]
     gdn.gdn_linear(d["x"], d["w_in"], M, N, d["hidden"], [(0, N, d["qkv"], N, 0)], stream)

@@ -249,7 +249,7 @@ def make_block_inputs(shape: Shape, hidden: int, seed: int = 0) -> dict:
 
 
 def make_attention_inputs(n_batch: int, n_tok: int, hidden: int, n_q: int, n_kv: int, d: int, seed: int = 0) -> dict:
-    """Inputs of one full-attention layer call: x [B][T][hidden] ~ N(0, 1), w_in [(n_q + 2 n_kv) d][hidden] ~
+    """Inputs of one device.attention_step: x [B][T][hidden] ~ N(0, 1), w_in [(n_q + 2 n_kv) d][hidden] ~
     N(0, 1/hidden) (the q, k and v projections, one output feature per row) and w_out [hidden][n_q d] ~
     N(0, 1/(n_q d)), all bf16-rounded."""
     rng = np.random.default_rng([seed, 2])

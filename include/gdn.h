@@ -465,10 +465,11 @@ int gdn_rope_init(const gdn_rope_params *params, gdn_rope_table *table);
  * the rotation is in 32 bits, rounded once.  positions: device int32 [n_axes][n_tok], any value.
  * x[s] and out[s]: rows of d channels (rot_dim <= d <= 256) with equal n_heads; in place if they
  * name the same memory with the same strides and type, otherwise they must not overlap, nor may one
- * segment's out and another segment's rows.  Types of x and out may differ.  n_tok == 0 is a no-op (positions and ptr may then be NULL).  Errors: NULL ->
- * GDN_ERR_ARG; n_segs, n_heads (1 .. 8192) or d out of range -> GDN_ERR_SHAPE; n_tok < 0 ->
- * GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE; same pointer with other strides or types, a pointer not
- * aligned to its elements, a table that gdn_rope_init did not make -> GDN_ERR_ARG.
+ * segment's out and another segment's rows.  Types of x and out may differ.  n_tok == 0 is a no-op
+ * (positions and ptr may then be NULL).  Errors: NULL -> GDN_ERR_ARG; n_segs, n_heads (1 .. 8192) or d out
+ * of range -> GDN_ERR_SHAPE; n_tok < 0 -> GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE; same pointer with other
+ * strides or types, a pointer not aligned to its elements, a table that gdn_rope_init did not make ->
+ * GDN_ERR_ARG.
  */
 int gdn_rope(const gdn_rope_table *table, const gdn_rows *x, const gdn_rows *out, int32_t n_segs,
              int32_t d, const int32_t *positions, int32_t n_tok, int32_t inverse, void *stream);
@@ -479,8 +480,8 @@ int gdn_rope(const gdn_rope_table *table, const gdn_rows *x, const gdn_rows *out
  * aligned; the 8-bit formats keep one fp32 scale per token and head, k_scale and v_scale
  * [n_pages][n_kv][page_size] (NULL for GDN_KV_BF16): value = code * scale, scale = max |x| / 448
  * (e4m3) or / 127 (i8), code = x * (1 / scale) rounded to nearest, ties to even.  A row of zeros, or of
- * values so small that 1 / scale overflows, has codes and scale 0.  A row that holds an infinity or a NaN gets codes 0 and scale NaN, so that every value of
- * it reads back as NaN.  flags: GDN_F_CHECK_INDICES or 0.
+ * values so small that 1 / scale overflows, has codes and scale 0.  A row that holds an infinity or a NaN
+ * gets codes 0 and scale NaN, so that every value of it reads back as NaN.  flags: GDN_F_CHECK_INDICES or 0.
  */
 enum gdn_kv_format { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1, GDN_KV_I8 = 2 };
 typedef struct gdn_kv {
@@ -537,7 +538,8 @@ int gdn_kv_read(const gdn_kv *kv, const gdn_kv_batch *batch, const gdn_rows *k, 
  * entry the cache rows of nodes path[b][0 .. n_path[b]) (device int32 [n_batch][max_path], strictly
  * increasing node indices) move to positions start[b], start[b] + 1, ...; codes and scales are
  * copied bit for bit.  n_path[b] is taken as at most max_path.  batch->n_tok is the tree's node count
- * (n_new[b], where given, that of entry b's); a path entry that is not a node index, or is below its own place in the path, is skipped.  As in
+ * (n_new[b], where given, that of entry b's); a path entry that is not a node index, or is below its own
+ * place in the path, is skipped.  As in
  * gdn_kv_write, two entries must not have the same places there.
  */
 int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *path,
@@ -556,16 +558,17 @@ int gdn_kv_commit(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *pa
  * Scores, maxima and sums are in fp32; for the product with v the weights are rounded to fp16 (8 bits:
  * 2^-11 of a weight times v scale down to 2^-21 of the row's largest, then 2^-32 of the largest), or (bf16
  * cache) to bf16, in two parts, hi and lo, where at most 64 rows share their keys.  A key that a row does
- * not see does not reach it, whatever its k and v hold.  A row whose keys are all on pages outside the pool is zero.  Scales of an 8-bit cache are not
- * negative; a v scale below 2^-64, 0 among them, counts as 2^-64, and counted so those of the keys of a
- * call lie within 2^100 of each other.
+ * not see does not reach it, whatever its k and v hold.  A row whose keys are all on pages outside the
+ * pool is zero.  Scales of an 8-bit cache are not negative; a v scale below 2^-64, 0 among them, counts as
+ * 2^-64, and counted so those of the keys of a call lie within 2^100 of each other.
  *   q, out: rows of n_q heads (a multiple of kv->n_kv) of d channels, GDN_BF16, aligned as in
- *   gdn_kv_write; out may be q itself, with the same strides, otherwise they must not overlap.  scale: > 0, scale log2(e) finite in fp32.
+ *   gdn_kv_write; out may be q itself, with the same strides, otherwise they must not overlap.
+ *   scale: > 0, scale log2(e) finite in fp32.
  *   workspace: device memory of gdn_attn_workspace_bytes, 16-byte aligned, needs no initialisation;
  *   calls (and recorded graphs) that may run at the same time need one each.
  * Errors: as gdn_kv_write; a workspace that is missing, misaligned or too small, a bad scale, or out on
- * q's memory with other strides -> GDN_ERR_ARG; sizes whose key tiles would pass 2^31, a table or prefix of 2^31 - max(n_tok, 64) positions or
- * more, or n_batch n_tok n_q / n_kv >= 2^26 -> GDN_ERR_SHAPE.
+ * q's memory with other strides -> GDN_ERR_ARG; sizes whose key tiles would pass 2^31, a table or prefix of
+ * 2^31 - max(n_tok, 64) positions or more, or n_batch n_tok n_q / n_kv >= 2^26 -> GDN_ERR_SHAPE.
  */
 int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *parent,
                     const int32_t *prefix_pages, int32_t max_prefix_pages, const int32_t *prefix_len,
