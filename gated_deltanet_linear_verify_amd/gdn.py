@@ -508,6 +508,8 @@ def gdn_attn_verify(kv: KvCache, q, block_table, start, n_new, parent, prefix_pa
     plen = None if prefix_len is None else _ints(fn, "prefix_len", prefix_len, here, T, 1)
     if workspace.get_device() != here:
         raise _elsewhere(fn, workspace, here)
+    if not workspace.is_contiguous():  # an expanded tensor has less memory than elements
+        raise _bad("gdn_attn_verify: workspace must be contiguous")
     _check(lib().gdn_attn_verify(kv.c, b, par, pre, 0 if pre is None else prefix_pages.shape[0], plen,
                                  _rows(fn, "q", q, here, T, n, d), _rows(fn, "out", out, here, T, n, d), scale,
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),

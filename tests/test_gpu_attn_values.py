@@ -198,3 +198,15 @@ def test_index_check_refuses_paths_of_nodes_that_do_not_count():
     k.copy_(before)
     commit(None)
     assert not torch.equal(k, before)
+
+
+def test_workspace_must_be_memory_of_its_size():
+    """A tensor expanded to the bytes that are needed, and a strided one, are refused before anything is launched."""
+    c = Case("bf16", 64, 1, 1, 16, [20], 1, seed=1).upload()
+    need = c.ws.numel()
+    for ws in (torch.zeros(16, dtype=torch.uint8, device="cuda")[:1].expand(need),
+               torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(gdn.GdnError) as e:
+            c.run(workspace=ws)
+        assert e.value.code == gdn.GDN_ERR_ARG
+    assert (c.out == 7.0).all()
