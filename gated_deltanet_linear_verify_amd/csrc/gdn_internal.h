@@ -212,6 +212,49 @@ bool attn_plan(int d, int format, int page_size, int n_kv, int grp, int n_batch,
                int max_prefix_pages, AttnPlan &p);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
 
+// ---- norms, products with an epilogue, log probabilities ----
+enum { kF32 = 0, kBf16 = 1, kE4m3 = 2, kI8 = 3 };  // gdn_dtype
+constexpr int kNormMaxD = 16384;
+struct NormArgs {
+    RowsView x, residual, total, out;  // residual.p, total.p NULL: none; out.bf16 counts for out_type F32 and BF16 only
+    const float *weight;               // or NULL
+    float *scale;                      // 8-bit out
+    int32_t out_type;
+    int32_t d, n_heads, n_tok, rms;
+    float eps;
+};
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
+
+struct MatView {
+    void *p;
+    const float *scale;
+    int64_t ld;
+    int32_t type;
+};
+struct LinearActArgs {
+    MatView x, w, residual, out;  // residual.p NULL: none
+    const float *bias;            // or NULL
+    int32_t M, N, K, act, gated;  // N: columns of out
+    int32_t splits;               // parts of K, each summed apart (set by the launcher)
+    unsigned char *ws;            // the parts' sums where splits > 1
+};
+size_t linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int type, bool gated);
+hipError_t launch_linear_act(const LinearActArgs &a, hipStream_t stream);
+
+constexpr int kMaxTop = 64, kMaxIds = 64;
+struct LogprobArgs {
+    const void *logits;
+    int64_t ld;
+    int32_t bf16, n_rows, V, n_ids, top_k;
+    float inv_t;                  // 1 / temperature
+    const int32_t *ids;
+    float *logprob, *lse, *entropy, *top_logprob;
+    int32_t *rank, *top_ids;
+    unsigned char *ws;
+};
+size_t logprob_workspace_bytes(int64_t n_rows, int V, bool bf16, int n_ids, int top_k);
+hipError_t launch_logprob(const LogprobArgs &a, hipStream_t stream);
+
 // Checks shared by the cache's entry points (gdn_kv_abi.cpp); each sets the last error.
 int abi_check_kv(const char *fn, const gdn_kv *kv, bool pointers);
 int abi_check_rows(const char *fn, const char *what, const gdn_rows *r, int n_heads);  // aligned rows

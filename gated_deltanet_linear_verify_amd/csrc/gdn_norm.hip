@@ -1,0 +1,231 @@
+// gdn_norm.hip - the norm between a layer's mixers (gfx950): s = x + residual, y = s / sqrt(mean(s^2) + eps) * w, in
+// 32 or 16 bits, or in 8 with one scale per row (lucebox-hub internal.h, struct TargetLayer: a layer's norms, q_norm
+// and k_norm; struct TargetWeights: rms_eps).
+//
+// A row stays in registers between its one read and its one write.  The row's scale needs max |y|, which is
+// max |s w| times the row's factor r = 1 / sqrt(mean(s^2) + eps): y is formed as (s w) r, and the rounding of a product with
+// one factor keeps the order, so max |y| is the rounded max |s w| r exactly.  The two reductions, sum s^2 and max |s w|, are
+// therefore one round between the lanes, and one exchange through LDS for rows of several waves.
+#include "gdn_rows.h"
+
+namespace gdn {
+
+namespace {
+
+// The sum of a and the maximum of the bits b over the TPR neighbouring lanes that share a row (8 .. 64): within quads, then
+// mirrored halves of 8 and 16 lanes by DPP, then rows of 16.
+template <int CTRL>
+__device__ __forceinline__ void dpp_reduce(float &a, uint32_t &b)
+{
+    a += dpp_mov<CTRL>(a);
+    b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false));
+}
+template <int TPR>
+__device__ __forceinline__ void lanes_reduce(float &a, uint32_t &b)
+{
+    dpp_reduce<0xB1>(a, b);                          // quad_perm [1,0,3,2]
+    dpp_reduce<0x4E>(a, b);                          // quad_perm [2,3,0,1]
+    dpp_reduce<0x141>(a, b);                         // row_half_mirror
+    if constexpr (TPR >= 16) dpp_reduce<0x140>(a, b);  // row_mirror
+#pragma unroll
+    for (int o = 16; o < TPR; o *= 2) {
+        a += __shfl_xor(a, o);
+        b = max(b, (uint32_t)__shfl_xor((int)b, o));
+    }
+}
+
+// W channels per chunk (8 where every row is aligned for it, else 1), PER chunks per thread.  TPR > 0: a row is TPR
+// neighbouring lanes of a wave, 256 / TPR rows to a workgroup; TPR == 0: a row is a workgroup.
+template <int W, int PER, int TPR>
+__global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
+{
+#pragma clang fp contract(off)  // y is the rounded product (s w) r, a code the rounded y (1 / scale)
+    __shared__ float sums[16];
+    __shared__ uint32_t tops[16];
+    const int rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
+    const int tpr = TPR ? TPR : (int)blockDim.x;
+    const int li = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
+    const int64_t n_rows = (int64_t)a.n_tok * a.n_heads;
+    int64_t row = (int64_t)blockIdx.x * rpw + (TPR ? threadIdx.x / (TPR ? TPR : 1) : 0);
+    const bool live = row < n_rows;
+    if (!live) row = n_rows - 1;  // lanes past the end follow the last row and store nothing
+    const int64_t t = row / a.n_heads, h = row % a.n_heads;
+    const int64_t xat = t * a.x.ld + h * a.x.hd;
+
+    float v[PER][W], w[PER][W];
+    const int d = a.d;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int c = (li + i * tpr) * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            v[i][j] = 0.0f;
+            w[i][j] = 1.0f;
+        }
+        if (c < d) {
+            load_row<W>(a.x.p, xat + c, a.x.bf16, v[i]);
+            if (a.weight) load_row<W>(a.weight, c, false, w[i]);
+        }
+    }
+    if (a.residual.p) {
+        const int64_t at = t * a.residual.ld + h * a.residual.hd;
+        float u[PER][W];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = (li + i * tpr) * W;
+            if (c < d) {
+                load_row<W>(a.residual.p, at + c, a.residual.bf16, u[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) u[i][j] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[i][j] += u[i][j];
+    }
+    if (a.total.p && live) {
+        const int64_t at = t * a.total.ld + h * a.total.hd;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = (li + i * tpr) * W;
+            if (c < d) store_row<W>(a.total.p, at + c, a.total.bf16, v[i]);
+        }
+    }
+
+    // one round between the lanes of a row: the sum of q, and the largest of the bits
+    auto round = [&](float &q, uint32_t &top) {
+        if constexpr (TPR > 0) {
+            lanes_reduce<TPR>(q, top);
+        } else {
+            lanes_reduce<64>(q, top);
+            const int wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6, o = threadIdx.x & 15;
+            __syncthreads();  // the last round's values have been read
+            if ((threadIdx.x & 63) == 0) {
+                sums[wave] = q;
+                tops[wave] = top;
+            }
+            __syncthreads();
+            q = o < n_waves ? sums[o] : 0.0f;
+            top = o < n_waves ? tops[o] : 0u;
+            lanes_reduce<16>(q, top);
+        }
+    };
+    // sum s^2, and max |s w| by its bits (ordered like the values, infinity and the NaNs above all)
+    auto measure = [&](float &q, uint32_t &top, bool weighed) {
+        q = 0.0f;
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                q = __builtin_fmaf(v[i][j], v[i][j], q);
+                top = max(top, __float_as_uint(weighed ? v[i][j] * w[i][j] : v[i][j]) & 0x7fffffffu);
+            }
+        round(q, top);
+    };
+    float r = 1.0f, ssq = 0.0f;
+    uint32_t top = 0;
+    const bool codes = a.out_type == kE4m3 || a.out_type == kI8;
+    if (a.rms || codes) measure(ssq, top, true);
+    if (a.rms) {
+        const float n = (float)d;
+        r = 1.0f / sqrtf(ssq / n + a.eps);
+        if (!(ssq < __builtin_inff())) {  // the same for all lanes of a row
+            uint32_t big;
+            measure(ssq, big, false);
+            if (big < 0x7f800000u) {  // finite values: scaled by the power of two that puts the largest in [1, 2)
+                const int e = (int)(big >> 23) - 127;
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[i][j] = ldexpf(v[i][j], -e);
+                measure(ssq, top, true);
+                r = 1.0f / sqrtf(ssq / n + ldexpf(a.eps, -2 * e));
+            }
+        }
+    }
+    const int64_t oat = t * a.out.ld + h * a.out.hd;
+    if (a.out_type == kF32 || a.out_type == kBf16) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = (li + i * tpr) * W;
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[i][j] = v[i][j] * w[i][j] * r;
+            if (c < d && live) store_row<W>(a.out.p, oat + c, a.out.bf16, v[i]);
+        }
+        return;
+    }
+    const float most = __uint_as_float(top) * r, full = a.out_type == kE4m3 ? 448.0f : 127.0f;
+    const bool finite = most < __builtin_inff();  // neither infinite nor NaN
+    float scale = most / full, inv = 1.0f / scale;
+    if (!(inv < __builtin_inff())) scale = inv = 0.0f;  // a row of zeros, or of values whose 1 / scale overflows
+    if (!finite) {
+        scale = __builtin_nanf("");
+        inv = 0.0f;
+    }
+    unsigned char *to = static_cast<unsigned char *>(a.out.p) + oat;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int c = (li + i * tpr) * W;
+        if (c >= d || !live) continue;
+        uint32_t code[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float y = finite ? v[i][j] * w[i][j] * r * inv : 0.0f;
+            if (a.out_type == kE4m3)
+                code[j] = __builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0, false) & 0xff;
+            else  // |y| <= 127 (1 + 2^-22): adding 1.5 2^23 rounds to nearest, ties to even
+                code[j] = __float_as_uint(y + 12582912.0f) & 0xff;
+        }
+        if constexpr (W == 8) {
+            const uint32_t lo = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+            const uint32_t hi = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+            *reinterpret_cast<uint64_t *>(to + c) = lo | (uint64_t)hi << 32;
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) to[c + j] = (unsigned char)code[j];
+        }
+    }
+    if (li == 0 && live) a.scale[row] = scale;
+}
+
+template <int W, int PER, int TPR>
+hipError_t launch_as(const NormArgs &a, int threads, hipStream_t stream)
+{
+    const int64_t rows = (int64_t)a.n_tok * a.n_heads, rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
+    hipLaunchKernelGGL((norm_kernel<W, PER, TPR>), dim3((unsigned)((rows + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int W>
+hipError_t launch_wide(const NormArgs &a, hipStream_t stream)
+{
+    const int chunks = (a.d + W - 1) / W;
+    if (chunks <= 8) return launch_as<W, 1, 8>(a, 256, stream);
+    if (chunks <= 16) return launch_as<W, 1, 16>(a, 256, stream);
+    if (chunks <= 32) return launch_as<W, 1, 32>(a, 256, stream);
+    if (chunks <= 64) return launch_as<W, 1, 64>(a, 256, stream);
+    if (chunks <= 1024) return launch_as<W, 1, 0>(a, (chunks + 63) / 64 * 64, stream);
+    if (chunks <= 2048) return launch_as<W, 2, 0>(a, ((chunks + 1) / 2 + 63) / 64 * 64, stream);
+    if constexpr (W == 1) {
+        if (chunks <= 4096) return launch_as<W, 4, 0>(a, 1024, stream);
+        return launch_as<W, 16, 0>(a, 1024, stream);
+    }
+    return hipErrorInvalidValue;  // d <= kNormMaxD = 2048 chunks of 8
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream)
+{
+    bool wide = a.d % 8 == 0 && (uintptr_t)a.weight % 16 == 0;
+    for (const RowsView *r : {&a.x, &a.residual, &a.total, &a.out}) {
+        const bool codes = r == &a.out && a.out_type >= kE4m3;
+        wide = wide && r->ld % 8 == 0 && r->hd % 8 == 0 && (uintptr_t)r->p % (codes ? 8 : 16) == 0;
+    }
+    return wide ? launch_wide<8>(a, stream) : launch_wide<1>(a, stream);
+}
+
+}  // namespace gdn

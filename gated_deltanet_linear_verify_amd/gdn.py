@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn.so")
 
 GDN_OK, GDN_ERR_ARG, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_RANGE, GDN_ERR_HIP = range(6)
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_E4M3, GDN_I8 = range(4)
 GDN_CHAIN, GDN_TREE = 0, 1
 GDN_F_QK_NORM_SILU = 0x1
 GDN_F_CHECK_INDICES = 0x2
@@ -23,12 +23,15 @@ GDN_F_DEFER_COMMIT = 0x4
 GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_YARN = range(4)
 GDN_KV_BF16, GDN_KV_E4M3, GDN_KV_I8 = range(3)
+GDN_NORM_RMS, GDN_NORM_NONE = 0, 1
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU, GDN_ACT_GELU_TANH, GDN_ACT_RELU, GDN_ACT_SIGMOID = range(6)
 
 EXPORTS = ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_batch", "gdn_rollback_trim",
            "gdn_prefill", "gdn_prefill_noalloc", "gdn_prefill_workspace_bytes", "gdn_capture_bytes", "gdn_reset",
            "gdn_snapshot", "gdn_restore", "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch",
            "gdn_graph_destroy", "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_bytes", "gdn_kv_write",
-           "gdn_kv_read", "gdn_kv_commit", "gdn_attn_verify", "gdn_attn_workspace_bytes", "gdn_last_error", "gdn_version")
+           "gdn_kv_read", "gdn_kv_commit", "gdn_attn_verify", "gdn_attn_workspace_bytes", "gdn_norm", "gdn_linear_act",
+           "gdn_linear_act_workspace_bytes", "gdn_logprob", "gdn_logprob_workspace_bytes", "gdn_last_error", "gdn_version")
 
 
 class GdnError(RuntimeError):
@@ -63,6 +66,10 @@ class gdn_out_seg(ctypes.Structure):
 class gdn_rows(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("ld", ctypes.c_int64), ("hd", ctypes.c_int64),
                 ("n_heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class gdn_mat(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class gdn_rope_params(ctypes.Structure):
@@ -139,11 +146,19 @@ def lib() -> ctypes.CDLL:
         L.gdn_attn_verify.argtypes = [K, B, P, P, I, P, R, R, ctypes.c_float, P, S, P]
         L.gdn_attn_workspace_bytes.argtypes = [K, I, I, I, I]
         L.gdn_attn_workspace_bytes.restype = S
+        A, F = ctypes.POINTER(gdn_mat), ctypes.c_float
+        L.gdn_norm.argtypes = [R, R, R, P, R, P, I, I, F, I, P]
+        L.gdn_linear_act.argtypes = [A, A, I, I, I, P, I, I, A, A, P, S, P]
+        L.gdn_linear_act_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.gdn_linear_act_workspace_bytes.restype = S
+        L.gdn_logprob.argtypes = [A, I, I, F, P, I, P, P, P, P, P, P, I, P, S, P]
+        L.gdn_logprob_workspace_bytes.argtypes = [I, I, I, I, I]
+        L.gdn_logprob_workspace_bytes.restype = S
         for f in ("gdn_verify", "gdn_verify_resume", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_batch",
                   "gdn_rollback_trim", "gdn_prefill", "gdn_prefill_noalloc", "gdn_reset", "gdn_snapshot", "gdn_restore",
                   "gdn_rollback_layers", "gdn_graph_create", "gdn_graph_launch", "gdn_graph_destroy",
                   "gdn_linear", "gdn_rope_init", "gdn_rope", "gdn_kv_write", "gdn_kv_read", "gdn_kv_commit",
-                  "gdn_attn_verify"):
+                  "gdn_attn_verify", "gdn_norm", "gdn_linear_act", "gdn_logprob"):
             getattr(L, f).restype = ctypes.c_int
         L.gdn_last_error.restype = ctypes.c_char_p
         L.gdn_version.restype = ctypes.c_char_p
@@ -191,7 +206,9 @@ class _Torch:
         import torch
         torch.cuda.current_device()  # initialises the runtime, or says why it cannot
         self.dtypes = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
-        self.int32 = torch.int32
+        self.codes = {torch.float8_e4m3fn: GDN_E4M3, torch.int8: GDN_I8}
+        self.all = {**self.dtypes, **self.codes}
+        self.int32, self.float32 = torch.int32, torch.float32
         self.device = torch.cuda.current_device
         self.stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -369,11 +386,11 @@ def _ints(fn: str, name: str, t, here: int, T: _Torch, n0: int, n1: int = -1) ->
     return t.data_ptr()
 
 
-def _rows(fn: str, name: str, t, here: int, T: _Torch, n_rows: int, d: int) -> gdn_rows:
+def _rows(fn: str, name: str, t, here: int, T: _Torch, n_rows: int, d: int, codes: bool = False) -> gdn_rows:
     """gdn_rows of a [n_rows][n_heads][d] tensor whose channels are contiguous (other strides are free)."""
     if t.get_device() != here:
         raise _elsewhere(fn, t, here)
-    dtype = T.dtypes.get(t.dtype)
+    dtype = (T.all if codes else T.dtypes).get(t.dtype)
     if dtype is None:
         raise GdnError(GDN_ERR_DTYPE, f"{fn}: {name} must be bfloat16 or float32, not {t.dtype}")
     shape, strides = t.shape, t.stride()
@@ -514,3 +531,101 @@ def gdn_attn_verify(kv: KvCache, q, block_table, start, n_new, parent, prefix_pa
                                  _rows(fn, "q", q, here, T, n, d), _rows(fn, "out", out, here, T, n, d), scale,
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                  T.stream(stream, here)))
+
+
+# ---- between the mixers and behind the last one: norms, products with an epilogue, log probabilities ----
+
+def _floats(fn: str, name: str, t, here: int, T: _Torch, n0: int, n1: int = -1) -> int:
+    """Address of a contiguous float32 tensor [n0] or [n0][n1] (the first size may be larger)."""
+    if t.get_device() != here:
+        raise _elsewhere(fn, t, here)
+    if t.dtype is not T.float32 or not t.is_contiguous():
+        raise _bad(f"{fn}: {name} must be a contiguous float32 tensor")
+    shape = t.shape
+    if len(shape) != (1 if n1 < 0 else 2) or shape[0] < n0 or (n1 >= 0 and shape[1] != n1):
+        raise _bad(f"{fn}: {name} has shape {tuple(shape)}, expected {(n0,) if n1 < 0 else (n0, n1)}")
+    return t.data_ptr()
+
+
+def _mat(fn: str, name: str, t, here: int, T: _Torch, rows: int, cols: int, types: dict, scale=None) -> gdn_mat:
+    """gdn_mat of a [rows][cols] tensor whose columns are contiguous (more rows are left alone)."""
+    if t.get_device() != here:
+        raise _elsewhere(fn, t, here)
+    dtype = types.get(t.dtype)
+    if dtype is None:
+        raise GdnError(GDN_ERR_DTYPE, f"{fn}: {name} must be one of {list(types)}, not {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (strides[1] != 1 and cols > 1):
+        raise _bad(f"{fn}: {name} must be [{rows}][{cols}] with contiguous columns, got {tuple(shape)} with strides {strides}")
+    return gdn_mat(t.data_ptr(), None if scale is None else _floats(fn, name + "_scale", scale, here, T, rows),
+                   strides[0] if shape[0] > 1 else cols, dtype)
+
+
+def _scratch(fn: str, t, here: int) -> tuple:
+    """(address, bytes) of a workspace tensor, or nothing."""
+    if t is None:
+        return None, 0
+    if t.get_device() != here:
+        raise _elsewhere(fn, t, here)
+    if not t.is_contiguous():  # an expanded tensor has less memory than elements
+        raise _bad(f"{fn}: workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def gdn_norm(x, weight, out, n_tok: int, *, residual=None, total=None, scale=None, eps: float = 1e-6,
+             mode: int = GDN_NORM_RMS, stream=None) -> None:
+    """RMS norm of x (+ residual) [n_tok][heads][d] by weight (float32 [d], or None) into out: bfloat16, float32, or
+    float8_e4m3fn / int8 with scale float32 [n_tok][heads]; total receives x + residual."""
+    fn, T = "gdn_norm", _torch()
+    here = T.device()
+    d, heads = x.shape[-1], x.shape[1] if x.dim() == 3 else 0
+    r = [None if t is None else _rows(fn, n, t, here, T, n_tok, d, n == "out")
+         for n, t in (("x", x), ("residual", residual), ("total", total), ("out", out))]
+    _check(lib().gdn_norm(r[0], r[1], r[2], None if weight is None else _floats(fn, "weight", weight, here, T, d), r[3],
+                          None if scale is None else _floats(fn, "scale", scale, here, T, n_tok, heads), d, n_tok, eps, mode,
+                          T.stream(stream, here)))
+
+
+def gdn_linear_act_workspace_bytes(M: int, N: int, K: int, dtype, gated: bool = False) -> int:
+    """Of a gdn_linear_act call with x and w of the torch type ``dtype``."""
+    import torch
+    codes = {torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_E4M3, torch.int8: GDN_I8}
+    return lib().gdn_linear_act_workspace_bytes(M, N, K, codes.get(dtype, -1), int(bool(gated)))
+
+
+def gdn_linear_act(x, w, out, M: int, N: int, K: int, *, x_scale=None, w_scale=None, bias=None, act: int = GDN_ACT_NONE,
+                   gated: bool = False, residual=None, workspace=None, stream=None) -> None:
+    """out [M][N] = act(x w^T + bias) + residual, or act(gate) * up of w's first and last N rows where gated; x [M][K] and
+    w [N or 2 N][K] in bfloat16, or float8_e4m3fn or int8 with float32 scales per row."""
+    fn, T, rows = "gdn_linear_act", _torch(), 2 * N if gated else N
+    here = T.device()
+    ws, ws_bytes = _scratch(fn, workspace, here)
+    _check(lib().gdn_linear_act(
+        _mat(fn, "x", x, here, T, M, K, T.all, x_scale), _mat(fn, "w", w, here, T, rows, K, T.all, w_scale), M, N, K,
+        None if bias is None else _floats(fn, "bias", bias, here, T, rows), act, 1 if gated else 0,
+        None if residual is None else _mat(fn, "residual", residual, here, T, M, N, T.dtypes),
+        _mat(fn, "out", out, here, T, M, N, T.dtypes), ws, ws_bytes, T.stream(stream, here)))
+
+
+def gdn_logprob_workspace_bytes(n_rows: int, n_vocab: int, dtype, n_ids: int = 0, top_k: int = 0) -> int:
+    """Of a gdn_logprob call with logits of the torch type ``dtype``."""
+    import torch
+    codes = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+    return lib().gdn_logprob_workspace_bytes(n_rows, n_vocab, codes.get(dtype, -1), n_ids, top_k)
+
+
+def gdn_logprob(logits, n_rows: int, n_vocab: int, *, ids=None, temperature: float = 1.0, logprob=None, rank=None,
+                lse=None, entropy=None, top_ids=None, top_logprob=None, workspace=None, stream=None) -> None:
+    """Of logits [n_rows][n_vocab]: log probabilities and ranks of ids (int32 [n_rows][n_ids], -1: none), log sum exp,
+    entropy, and the first top_k alternatives (top_ids int32 and top_logprob [n_rows][top_k])."""
+    fn, T = "gdn_logprob", _torch()
+    here = T.device()
+    n_ids = 0 if ids is None else ids.shape[-1]
+    k = 0 if top_ids is None else top_ids.shape[-1]
+    at = lambda get, n, t, *sizes: None if t is None else get(fn, n, t, here, T, n_rows, *sizes)  # noqa: E731
+    ws, ws_bytes = _scratch(fn, workspace, here)
+    _check(lib().gdn_logprob(
+        _mat(fn, "logits", logits, here, T, n_rows, n_vocab, T.dtypes), n_rows, n_vocab, temperature,
+        at(_ints, "ids", ids, n_ids), n_ids, at(_floats, "logprob", logprob, n_ids), at(_ints, "rank", rank, n_ids),
+        at(_floats, "lse", lse), at(_floats, "entropy", entropy), at(_ints, "top_ids", top_ids, k),
+        at(_floats, "top_logprob", top_logprob, k), k, ws, ws_bytes, T.stream(stream, here)))

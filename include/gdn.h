@@ -65,7 +65,9 @@ enum gdn_status {
     GDN_ERR_HIP = 5     /* the HIP runtime reported an error */
 };
 
-enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 };
+/* GDN_E4M3 and GDN_I8 are codes of 8 bits that stand for code * scale, one fp32 scale per row; only gdn_norm's
+ * out and gdn_linear_act's x and w take them. */
+enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2, GDN_I8 = 3 };
 
 enum gdn_capture_mode { GDN_CHAIN = 0, GDN_TREE = 1 };
 
@@ -578,6 +580,99 @@ int gdn_attn_verify(const gdn_kv *kv, const gdn_kv_batch *batch, const int32_t *
  * invalid sizes.  It does not depend on the lengths in the cache. */
 size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n_batch, int32_t n_tok,
                                 int32_t prefix);
+
+/*
+ * What stands between a layer's mixers and behind the last one: the norm with the residual's addition, the FFN's
+ * products, and what the step answers with.
+ *
+ * gdn_norm: root-mean-square norm of rows of heads (lucebox-hub internal.h, struct TargetLayer and struct
+ * TargetWeights: the norms of a layer, q_norm and k_norm, rms_eps), with the residual's addition before it and a
+ * rounding to 8 bits behind it.  For every token and head, over its d channels:
+ *   s = x + residual          (residual NULL: s = x);  total, if not NULL, receives s
+ *   y = s / sqrt(mean(s^2) + eps) * weight             (weight NULL: ones)
+ *   out = y; in 8 bits scale = max |y| / 448 (GDN_E4M3) or / 127 (GDN_I8) and code = y * (1 / scale), rounded to
+ *   nearest, ties to even
+ * mode GDN_NORM_NONE leaves the division out: y = s * weight (what a caller wants that only adds or rounds to 8 bits).
+ * Sums are in fp32 and y is formed from the s before its rounding; total and out are each rounded once.  Rows whose
+ * squares pass fp32's range are scaled first, so that every finite row has its norm.  A row of zeros, or of values so
+ * small that 1 / scale overflows, has codes and scale 0; a row of y that holds an infinity or a NaN gets codes 0 and
+ * scale NaN, as in gdn_kv_write.
+ *   x, residual, total: rows of equal n_heads (1 .. 8192), GDN_F32 or GDN_BF16, aligned to their elements; a token's
+ *   heads may lie inside wider rows.  out: also GDN_E4M3 and GDN_I8; scale: fp32 [n_tok][n_heads], given for those
+ *   types only.  total may be x or residual, and out may be x, residual or (not in 8 bits) nothing else, in place: with
+ *   the same strides and type.  Otherwise what is written must not overlap anything else of the call.
+ *   d 1 .. 16384; n_tok >= 0 (0 is a no-op), n_tok * n_heads <= 2^26; eps >= 2^-126 and finite.
+ * Errors: NULL x or out, a scale that is missing or given for the wrong type, a pointer that is not aligned to its
+ * elements, the same pointer with other strides or types, rows to write that overlap themselves, bad eps or mode ->
+ * GDN_ERR_ARG; d, n_heads, too many rows -> GDN_ERR_SHAPE; n_tok < 0 -> GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE.
+ */
+enum gdn_norm_mode { GDN_NORM_RMS = 0, GDN_NORM_NONE = 1 };
+int gdn_norm(const gdn_rows *x, const gdn_rows *residual, const gdn_rows *total, const float *weight, const gdn_rows *out,
+             float *scale, int32_t d, int32_t n_tok, float eps, int32_t mode, void *stream);
+
+/* A matrix by rows: element (r, c) is ptr[r * ld + c]; scale: one fp32 per row, for the 8-bit types only. */
+typedef struct gdn_mat {
+    void *ptr;
+    const float *scale;
+    int64_t ld;      /* elements from one row to the next */
+    int32_t dtype;   /* gdn_dtype */
+} gdn_mat;
+
+enum gdn_act {
+    GDN_ACT_NONE = 0,
+    GDN_ACT_SILU = 1,      /* v / (1 + e^-v) */
+    GDN_ACT_GELU = 2,      /* v / 2 (1 + erf(v / sqrt(2))) */
+    GDN_ACT_GELU_TANH = 3, /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+    GDN_ACT_RELU = 4,      /* max(v, 0); a NaN stays one */
+    GDN_ACT_SIGMOID = 5    /* 1 / (1 + e^-v) */
+};
+/*
+ * A product with its epilogue (an FFN's gate, up and down products, an output projection with its residual, a
+ * vocabulary's logits):  with p[m][n] = x.scale[m] w.scale[n] sum_k x[m][k] w[n][k] + bias[n],
+ *   out[m][n] = act(p[m][n]) + residual[m][n]                    gated == 0: w has N rows, bias N values
+ *   out[m][n] = act(p[m][n]) p[m][N + n] + residual[m][n]        gated != 0: w has 2 N rows, bias 2 N values
+ * x [M][K] and w [N or 2 N][K] are both GDN_BF16 (without scales), both GDN_E4M3 or both GDN_I8 (with them).  The sum
+ * over k is in fp32 (for GDN_I8 in int32, exact), the epilogue in fp32, rounded once to out's type.  bias (fp32) and
+ * residual may be NULL.  out and residual [M][N] are GDN_F32 or GDN_BF16, aligned to their elements; residual may be
+ * out itself (same stride and type), otherwise nothing may overlap out.
+ *   x and w: 16-byte aligned with rows that keep that alignment; K a multiple of 8 (GDN_BF16) or 16 (8 bits), for
+ *   GDN_I8 below 2^17.  M >= 0 (0 is a no-op), N, K >= 1, each below 2^26.
+ *   workspace: device memory of gdn_linear_act_workspace_bytes (NULL where that is 0), 16-byte aligned, needs no
+ *   initialisation; calls (and recorded graphs) that may run at the same time need one each.
+ * Errors: NULL, misalignment, scales missing or given for the wrong type, out's rows on top of each other, out on
+ * residual's memory with another stride or type, a workspace that is missing or too small, unknown act -> GDN_ERR_ARG;
+ * sizes -> GDN_ERR_SHAPE; M < 0 -> GDN_ERR_RANGE; types -> GDN_ERR_DTYPE.
+ */
+int gdn_linear_act(const gdn_mat *x, const gdn_mat *w, int32_t M, int32_t N, int32_t K, const float *bias, int32_t act,
+                   int32_t gated, const gdn_mat *residual, const gdn_mat *out, void *workspace, size_t ws_bytes, void *stream);
+/* Workspace bytes of a gdn_linear_act call with these sizes and x's type; 0 where it needs none, or on invalid sizes. */
+size_t gdn_linear_act_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t gated);
+
+/*
+ * What a verify step answers with (hf2q qwen35_target.rs, forward_decode_verify_batched: the logits of every position
+ * and their argmax, the first of equal ones): for every row of logits [n_rows][n_vocab] (GDN_F32 or GDN_BF16), with
+ * l = logits / temperature,
+ *   lse[r] = log sum_j e^l_j,   entropy[r] = -sum_j p_j log p_j with p = e^(l - lse)
+ *   logprob[r][i] = l_id - lse  and  rank[r][i] = how many logits are before it in the order below, for the given
+ *     tokens id = ids[r][i] (device int32 [n_rows][n_ids]: the drafted token, a tree node's children); an id outside
+ *     [0, n_vocab) (-1: none) has logprob -infinity and rank -1
+ *   top_ids[r][0 .. top_k) and top_logprob: the first top_k tokens in that order and their log probabilities
+ * The order: larger logits first, of equal ones the lower index; a NaN counts as -infinity in it, and -0 as 0.  Rank 0 is the argmax.
+ * Logits of -infinity (masked tokens) have probability 0 and add nothing; a row of nothing else has lse and log
+ * probabilities -infinity and entropy 0.  A row that holds a NaN or +infinity has NaN for lse, entropy and the log
+ * probabilities of valid tokens.  Every output is optional (NULL); logprob and rank need ids, and top_ids and top_logprob come together.
+ * Sums are in fp32; every logit is read once, beside those of the given tokens.
+ *   logits: aligned to their elements, any row stride.  n_rows 0 .. 2^26 (0 is a no-op); n_vocab 1 .. 2^24;
+ *   n_ids 0 .. 64; top_k 0 .. min(64, n_vocab); temperature: from 2^-20 to 2^20.
+ *   workspace: as gdn_linear_act's, of gdn_logprob_workspace_bytes.
+ * Errors: NULL logits, misalignment, ids missing or nothing asked of them, one of top_ids and top_logprob without the
+ * other or without top_k, no output at all, bad temperature or workspace -> GDN_ERR_ARG; sizes -> GDN_ERR_SHAPE; n_rows < 0 ->
+ * GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE.
+ */
+int gdn_logprob(const gdn_mat *logits, int32_t n_rows, int32_t n_vocab, float temperature, const int32_t *ids, int32_t n_ids,
+                float *logprob, int32_t *rank, float *lse, float *entropy, int32_t *top_ids, float *top_logprob, int32_t top_k,
+                void *workspace, size_t ws_bytes, void *stream);
+size_t gdn_logprob_workspace_bytes(int32_t n_rows, int32_t n_vocab, int32_t dtype, int32_t n_ids, int32_t top_k);
 
 /* Thread-local description of the last error of this thread ("" after success).  The pages'
  * header keeps one error-reporting channel that its loaders and graph builders write to, with
