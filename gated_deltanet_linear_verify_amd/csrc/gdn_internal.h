@@ -244,7 +244,7 @@ hipError_t launch_linear_act(const LinearActArgs &a, hipStream_t stream);
 constexpr int kMaxTop = 64, kMaxIds = 64;
 struct LogprobArgs {
     const void *logits;
-    int64_t ld;
+    int64_t ld, row0;             // row0: first row of one launch (set by the launcher)
     int32_t bf16, n_rows, V, n_ids, top_k;
     float inv_t;                  // 1 / temperature
     const int32_t *ids;
