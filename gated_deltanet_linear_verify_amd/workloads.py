@@ -266,3 +266,24 @@ def tree_path(parent: np.ndarray, node: int) -> list:
         path.append(int(node))
         node = int(parent[node])
     return path[::-1]
+
+
+def make_ffn_inputs(n_rows: int, hidden: int, width: int, seed: int = 0) -> dict:
+    """Inputs of one device.ffn_step: x [M][hidden] ~ N(0, 1) and the weights w_gate_up [2 width][hidden] (gate rows,
+    then up rows) ~ N(0, 1/hidden) and w_down [hidden][width] ~ N(0, 1/width), bf16-rounded; stream [M][hidden] ~
+    N(0, 3) and norm_w = 1 + N(0, 0.1) in fp32."""
+    rng = np.random.default_rng([seed, 3])
+    return {"x": round_to(rng.standard_normal((n_rows, hidden)), BF16),
+            "w_gate_up": round_to(rng.normal(0.0, hidden ** -0.5, (2 * width, hidden)), BF16),
+            "w_down": round_to(rng.normal(0.0, width ** -0.5, (hidden, width)), BF16),
+            "stream": round_to(rng.normal(0.0, 3.0, (n_rows, hidden)), F32),
+            "norm_w": round_to(1.0 + rng.normal(0.0, 0.1, hidden), F32)}
+
+
+def make_head_inputs(n_rows: int, hidden: int, vocab: int, seed: int = 0) -> dict:
+    """Inputs of one device.head_step: stream [M][hidden] ~ N(0, 3) and norm_w = 1 + N(0, 0.1) in fp32, and the
+    vocabulary's weight w [vocab][hidden] ~ N(0, 6/hidden), bf16-rounded."""
+    rng = np.random.default_rng([seed, 4])
+    return {"stream": round_to(rng.normal(0.0, 3.0, (n_rows, hidden)), F32),
+            "norm_w": round_to(1.0 + rng.normal(0.0, 0.1, hidden), F32),
+            "w": round_to(rng.normal(0.0, (6.0 / hidden) ** 0.5, (vocab, hidden)), BF16)}

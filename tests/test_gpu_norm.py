@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-import layer_ref as ref
+from tests import layer_ref as ref
 from gated_deltanet_linear_verify_amd import gdn
 
 pytestmark = pytest.mark.gpu
