@@ -221,6 +221,7 @@ struct NormArgs {
     float *scale;                      // 8-bit out
     int32_t out_type;
     int32_t d, n_heads, n_tok, rms;
+    int64_t row0;  // first row of one launch (set by the launcher)
     float eps;
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream);

@@ -411,7 +411,7 @@ __global__ __launch_bounds__(64 * GM * GN, WM * WN <= 8 ? 2 : 1) void linear_act
     constexpr int STEP = GATED ? 2 : 1, QUADS = 8 * WN, OUT = QUADS / STEP;
     constexpr int PASSES = (BM * BN * 4 + NBUF * BUF - 1) / (NBUF * BUF), ROWS = 32 * WM / PASSES;  // rows of a pass
     static_assert(WM % PASSES == 0, "passes of whole tiles");
-    constexpr int STRIDE = 64 / OUT, AT = ROWS / STRIDE < 4 ? ROWS / STRIDE : 4;  // rows of a store, and stores at a time
+    constexpr int STRIDE = 64 / OUT, AT = ROWS / STRIDE < 4 ? ROWS / STRIDE : GM * GN > 8 ? 2 : 4;  // rows of a store, and stores at a time
     static_assert(64 % OUT == 0 && ROWS % STRIDE == 0 && ROWS / STRIDE % AT == 0, "whole rows");
     const int c = lane % OUT, r0 = lane / OUT, first = GATED ? (c >> 2) * 8 + (c & 3) : c;
     const int n = n0 + 32 * WN / STEP * wn + 4 * c;
@@ -515,6 +515,7 @@ hipError_t launch_tile(const LinearActArgs &a, int wide, hipStream_t stream)
 {
     constexpr int BM = 32 * WM * GM, BN = 32 * WN * GN, CB = GATED ? BN / 2 : BN;
     const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + CB - 1) / CB);
+    if (tiles * 64 * GM * GN > 0xffffffffll) return hipErrorInvalidValue;  // a launch's x axis holds fewer than 2^32 threads
     hipLaunchKernelGGL((linear_act_kernel<T, GATED, GM, GN, WM, WN, NBUF, PIPE, SHORT>), dim3((unsigned)tiles, a.splits), dim3(64 * GM * GN),
                        NBUF * ((SHORT ? 16 : BM) + BN) * kRowBytes, stream, a, wide);
     if (hipError_t e = hipGetLastError()) return e;

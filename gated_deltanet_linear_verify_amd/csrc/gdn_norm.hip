@@ -46,7 +46,7 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
     const int tpr = TPR ? TPR : (int)blockDim.x;
     const int li = TPR ? threadIdx.x % (TPR ? TPR : 1) : threadIdx.x;
     const int64_t n_rows = (int64_t)a.n_tok * a.n_heads;
-    int64_t row = (int64_t)blockIdx.x * rpw + (TPR ? threadIdx.x / (TPR ? TPR : 1) : 0);
+    int64_t row = a.row0 + (int64_t)blockIdx.x * rpw + (TPR ? threadIdx.x / (TPR ? TPR : 1) : 0);
     const bool live = row < n_rows;
     if (!live) row = n_rows - 1;  // lanes past the end follow the last row and store nothing
     const int64_t t = row / a.n_heads, h = row % a.n_heads;
@@ -192,11 +192,16 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
 }
 
 template <int W, int PER, int TPR>
-hipError_t launch_as(const NormArgs &a, int threads, hipStream_t stream)
+hipError_t launch_as(NormArgs a, int threads, hipStream_t stream)
 {
     const int64_t rows = (int64_t)a.n_tok * a.n_heads, rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
-    hipLaunchKernelGGL((norm_kernel<W, PER, TPR>), dim3((unsigned)((rows + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
-    return hipGetLastError();
+    const int64_t run = (int64_t)0xffffffff / threads * rpw;  // rows of one launch: its x axis holds fewer than 2^32 threads
+    for (a.row0 = 0; a.row0 < rows; a.row0 += run) {
+        const int64_t n = rows - a.row0 < run ? rows - a.row0 : run;
+        hipLaunchKernelGGL((norm_kernel<W, PER, TPR>), dim3((unsigned)((n + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return hipSuccess;
 }
 
 template <int W>

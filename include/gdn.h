@@ -599,8 +599,8 @@ size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n_batch, 
  * scale NaN, as in gdn_kv_write.
  *   x, residual, total: rows of equal n_heads (1 .. 8192), GDN_F32 or GDN_BF16, aligned to their elements; a token's
  *   heads may lie inside wider rows.  out: also GDN_E4M3 and GDN_I8; scale: fp32 [n_tok][n_heads], given for those
- *   types only.  total may be x or residual, and out may be x, residual or (not in 8 bits) nothing else, in place: with
- *   the same strides and type.  Otherwise what is written must not overlap anything else of the call.
+ *   types only.  total and out may each be x or residual in place, with the same strides and type, but not both the same
+ *   one.  Otherwise what is written must not overlap anything else of the call.
  *   d 1 .. 16384; n_tok >= 0 (0 is a no-op), n_tok * n_heads <= 2^26; eps >= 2^-126 and finite.
  * Errors: NULL x or out, a scale that is missing or given for the wrong type, a pointer that is not aligned to its
  * elements, the same pointer with other strides or types, rows to write that overlap themselves, bad eps or mode ->
@@ -610,7 +610,7 @@ enum gdn_norm_mode { GDN_NORM_RMS = 0, GDN_NORM_NONE = 1 };
 int gdn_norm(const gdn_rows *x, const gdn_rows *residual, const gdn_rows *total, const float *weight, const gdn_rows *out,
              float *scale, int32_t d, int32_t n_tok, float eps, int32_t mode, void *stream);
 
-/* A matrix by rows: element (r, c) is ptr[r * ld + c]; scale: one fp32 per row, for the 8-bit types only. */
+/* A matrix by rows: element (r, c) is ptr[r * ld + c], any ld; scale: one fp32 per row, for the 8-bit types only. */
 typedef struct gdn_mat {
     void *ptr;
     const float *scale;
@@ -632,7 +632,10 @@ enum gdn_act {
  *   out[m][n] = act(p[m][n]) + residual[m][n]                    gated == 0: w has N rows, bias N values
  *   out[m][n] = act(p[m][n]) p[m][N + n] + residual[m][n]        gated != 0: w has 2 N rows, bias 2 N values
  * x [M][K] and w [N or 2 N][K] are both GDN_BF16 (without scales), both GDN_E4M3 or both GDN_I8 (with them).  The sum
- * over k is in fp32 (for GDN_I8 in int32, exact), the epilogue in fp32, rounded once to out's type.  bias (fp32) and
+ * over k is in fp32 (for GDN_I8 in int32, exact), the epilogue in fp32, rounded once to out's type.  With GDN_E4M3 and a
+ * GDN_BF16 out the products go through the 8-bit matrix instructions, which keep about 16 bits of each beside the largest
+ * they add it to (1.4e-5 of the result's norm, 1/120 of bf16's rounding); with a GDN_F32 out they are widened first and exact.
+ * The order of a sum, and with it the last bits, may differ between sizes, not between calls.  bias (fp32) and
  * residual may be NULL.  out and residual [M][N] are GDN_F32 or GDN_BF16, aligned to their elements; residual may be
  * out itself (same stride and type), otherwise nothing may overlap out.
  *   x and w: 16-byte aligned with rows that keep that alignment; K a multiple of 8 (GDN_BF16) or 16 (8 bits), for
