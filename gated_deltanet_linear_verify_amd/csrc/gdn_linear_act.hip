@@ -115,25 +115,37 @@ __device__ __forceinline__ float activate(int act, float v)
     }
 }
 
-// Column n of row m of out, from the sums p (and q of the up row).
-__device__ __forceinline__ void finish_one(const LinearActArgs &a, int64_t m, int n, float p, float q)
-{
-    const float sx = a.x.scale ? a.x.scale[m] : 1.0f;
-    float v = a.x.scale ? p * (sx * a.w.scale[n]) : p;
-    if (a.bias) v += a.bias[n];
-    v = activate(a.act, v);
-    if (a.gated) {
-        float u = a.x.scale ? q * (sx * a.w.scale[a.N + n]) : q;
-        if (a.bias) u += a.bias[a.N + n];
-        v *= u;
+// One column: what belongs to it is loaded once for many rows.
+struct Column {
+    float s = 1.0f, s2 = 1.0f, b = 0.0f, b2 = 0.0f;
+    int n;
+    __device__ Column(const LinearActArgs &a, int n_) : n(n_)
+    {
+        if (a.x.scale) s = a.w.scale[n];
+        if (a.bias) b = a.bias[n];
+        if (!a.gated) return;
+        if (a.x.scale) s2 = a.w.scale[a.N + n];
+        if (a.bias) b2 = a.bias[a.N + n];
     }
-    const int64_t rat = m * a.residual.ld + n, at = m * a.out.ld + n;
-    if (a.residual.p) v += a.residual.type == kBf16 ? load_act<true>(a.residual.p, rat) : load_act<false>(a.residual.p, rat);
-    if (a.out.type == kBf16)
-        static_cast<__bf16 *>(a.out.p)[at] = (__bf16)v;
-    else
-        static_cast<float *>(a.out.p)[at] = v;
-}
+    // of row m, from the sums p (and q of the up row)
+    __device__ float value(const LinearActArgs &a, int64_t m, float p, float q) const
+    {
+        const float sx = a.x.scale ? a.x.scale[m] : 1.0f;
+        float v = activate(a.act, (a.x.scale ? p * (sx * s) : p) + b);
+        if (a.gated) v *= (a.x.scale ? q * (sx * s2) : q) + b2;
+        const int64_t at = m * a.residual.ld + n;
+        if (a.residual.p) v += a.residual.type == kBf16 ? load_act<true>(a.residual.p, at) : load_act<false>(a.residual.p, at);
+        return v;
+    }
+    __device__ void store(const LinearActArgs &a, int64_t m, float v) const
+    {
+        const int64_t at = m * a.out.ld + n;
+        if (a.out.type == kBf16)
+            static_cast<__bf16 *>(a.out.p)[at] = (__bf16)v;
+        else
+            static_cast<float *>(a.out.p)[at] = v;
+    }
+};
 
 // Four columns from n on (all below N) at once: what belongs to the columns is loaded once for many rows.
 struct Columns {
@@ -441,7 +453,8 @@ __global__ __launch_bounds__(64 * GM * GN, WM * WN <= 8 ? 2 : 1) void linear_act
                 *to = sums(r, first);
                 if constexpr (GATED) to[quads(a.N)] = sums(r, first + 4);
             }
-        } else if (wide && n + 4 <= a.N) {
+        } else if (wide) {  // N is a multiple of 4: a quad is inside or past the end
+            if (n >= a.N) continue;
             const Columns cols(a, n);
 #pragma unroll 1
             for (int it = 0; it < ROWS / STRIDE; it += AT) {  // AT rows' loads before the first is used
@@ -463,12 +476,27 @@ __global__ __launch_bounds__(64 * GM * GN, WM * WN <= 8 ? 2 : 1) void linear_act
                 }
             }
         } else {
+            // any alignment: a column per lane, a row (or a few) at a time
+            constexpr int COLS = 4 * OUT < 64 ? 4 * OUT : 64, DOWN = 64 / COLS, UP = GM * GN > 8 ? 1 : 4;
+            static_assert(4 * OUT <= 64 && ROWS % (DOWN * UP) == 0, "columns of a wave");
+            const int col = lane % COLS, quad = GATED ? (col >> 4) * 8 + (col >> 2 & 3) : col >> 2;
+            const int nc = n0 + 32 * WN / STEP * wn + col;
+            const Column one(a, min(nc, a.N - 1));
 #pragma unroll 1
-            for (int e = 0; e < ROWS / STRIDE * 4; ++e) {
-                const int r = e / 4 * STRIDE + r0, m = mp + r, k = e % 4;
-                const float *p = reinterpret_cast<const float *>(&mine[r * QUADS + (first ^ (r & 7))]);
-                const float *q = reinterpret_cast<const float *>(&mine[r * QUADS + ((GATED ? first + 4 : first) ^ (r & 7))]);
-                if (m < a.M && n + k < a.N) finish_one(a, m, n + k, p[k], q[k]);
+            for (int it = 0; it < ROWS / DOWN; it += UP) {
+                float v[UP];
+#pragma unroll
+                for (int k = 0; k < UP; ++k) {
+                    const int r = (it + k) * DOWN + lane / COLS;
+                    const float *p = reinterpret_cast<const float *>(&mine[r * QUADS + (quad ^ (r & 7))]);
+                    const float *q = reinterpret_cast<const float *>(&mine[r * QUADS + ((GATED ? quad + 4 : quad) ^ (r & 7))]);
+                    v[k] = one.value(a, min(mp + r, a.M - 1), p[col & 3], q[col & 3]);
+                }
+#pragma unroll
+                for (int k = 0; k < UP; ++k) {
+                    const int m = mp + (it + k) * DOWN + lane / COLS;
+                    if (m < a.M && nc < a.N) one.store(a, m, v[k]);
+                }
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -499,15 +527,17 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearActArgs a, int w
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[g][r] = (float)whole[r];
     }
-    if (wide && n + 4 <= a.N) {
+    if (wide) {
         const Columns cols(a, n);
         const float sx = a.x.scale ? a.x.scale[m] : 1.0f;
         const f4 res = cols.residual(a, m);
         cols.store(a, m, a.gated ? cols.value<true>(a, sx, s[0], s[1], res) : cols.value<false>(a, sx, s[0], s[0], res));
         return;
     }
-    for (int r = 0; r < 4; ++r)
-        if (n + r < a.N) finish_one(a, m, n + r, s[0][r], s[1][r]);
+    for (int r = 0; r < 4 && n + r < a.N; ++r) {
+        const Column one(a, n + r);
+        one.store(a, m, one.value(a, m, s[0][r], s[1][r]));
+    }
 }
 
 template <int T, bool GATED, int GM, int GN, int WM, int WN, int NBUF, bool PIPE = true, bool SHORT = false>

@@ -204,21 +204,29 @@ hipError_t launch_as(NormArgs a, int threads, hipStream_t stream)
     return hipSuccess;
 }
 
+// A row's threads: neighbouring lanes of a wave up to 64 chunks (single channels: up to 512, eight to a lane, as a load
+// of one channel is an instruction: 8191 x 24 heads of 129 channels 162 us with a thread each, 86 so), else a workgroup with
+// as few chunks to a thread as its 1024 threads allow (5120 channels of one token: one chunk each; single channels: 8 or 16,
+// 8191 x 5121 215 us against 286 with 16 in whole workgroups).
 template <int W>
 hipError_t launch_wide(const NormArgs &a, hipStream_t stream)
 {
     const int chunks = (a.d + W - 1) / W;
+    const auto threads = [&](int per) { return ((chunks + per - 1) / per + 63) / 64 * 64; };
     if (chunks <= 8) return launch_as<W, 1, 8>(a, 256, stream);
     if (chunks <= 16) return launch_as<W, 1, 16>(a, 256, stream);
     if (chunks <= 32) return launch_as<W, 1, 32>(a, 256, stream);
     if (chunks <= 64) return launch_as<W, 1, 64>(a, 256, stream);
-    if (chunks <= 1024) return launch_as<W, 1, 0>(a, (chunks + 63) / 64 * 64, stream);
-    if (chunks <= 2048) return launch_as<W, 2, 0>(a, ((chunks + 1) / 2 + 63) / 64 * 64, stream);
-    if constexpr (W == 1) {
-        if (chunks <= 4096) return launch_as<W, 4, 0>(a, 1024, stream);
-        return launch_as<W, 16, 0>(a, 1024, stream);
+    if constexpr (W == 8) {
+        if (chunks <= 1024) return launch_as<W, 1, 0>(a, threads(1), stream);
+        return launch_as<W, 2, 0>(a, threads(2), stream);  // d <= kNormMaxD = 2048 chunks of 8
+    } else {
+        if (chunks <= 128) return launch_as<W, 2, 64>(a, 256, stream);
+        if (chunks <= 256) return launch_as<W, 4, 64>(a, 256, stream);
+        if (chunks <= 512) return launch_as<W, 8, 64>(a, 256, stream);
+        if (chunks <= 8192) return launch_as<W, 8, 0>(a, threads(8), stream);
+        return launch_as<W, 16, 0>(a, threads(16), stream);
     }
-    return hipErrorInvalidValue;  // d <= kNormMaxD = 2048 chunks of 8
 }
 
 }  // namespace
