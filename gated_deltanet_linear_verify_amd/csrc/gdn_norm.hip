@@ -36,7 +36,7 @@ __device__ __forceinline__ void lanes_reduce(float &a, uint32_t &b)
 
 // W channels per chunk (8 where every row is aligned for it, else 1), PER chunks per thread.  TPR > 0: a row is TPR
 // neighbouring lanes of a wave, 256 / TPR rows to a workgroup; TPR == 0: a row is a workgroup.
-template <int W, int PER, int TPR>
+template <int W, int PER, int TPR, bool STREAM>
 __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
 {
 #pragma clang fp contract(off)  // y is the rounded product (s w) r, a code the rounded y (1 / scale)
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = (li + i * tpr) * W;
-            if (c < d) store_row<W>(a.total.p, at + c, a.total.bf16, v[i]);
+            if (c < d) store_row<W, STREAM>(a.total.p, at + c, a.total.bf16, v[i]);
         }
     }
 
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
             const int c = (li + i * tpr) * W;
 #pragma unroll
             for (int j = 0; j < W; ++j) v[i][j] = v[i][j] * w[i][j] * r;
-            if (c < d && live) store_row<W>(a.out.p, oat + c, a.out.bf16, v[i]);
+            if (c < d && live) store_row<W, STREAM>(a.out.p, oat + c, a.out.bf16, v[i]);
         }
         return;
     }
@@ -182,7 +182,11 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
         if constexpr (W == 8) {
             const uint32_t lo = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
             const uint32_t hi = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-            *reinterpret_cast<uint64_t *>(to + c) = lo | (uint64_t)hi << 32;
+            const uint64_t codes8 = lo | (uint64_t)hi << 32;
+            if constexpr (STREAM)
+                __builtin_nontemporal_store(codes8, reinterpret_cast<uint64_t *>(to + c));
+            else
+                *reinterpret_cast<uint64_t *>(to + c) = codes8;
         } else {
 #pragma unroll
             for (int j = 0; j < W; ++j) to[c + j] = (unsigned char)code[j];
@@ -191,14 +195,14 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
     if (li == 0 && live) a.scale[row] = scale;
 }
 
-template <int W, int PER, int TPR>
+template <int W, int PER, int TPR, bool STREAM = false>
 hipError_t launch_as(NormArgs a, int threads, hipStream_t stream)
 {
     const int64_t rows = (int64_t)a.n_tok * a.n_heads, rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
     const int64_t run = (int64_t)0xffffffff / threads * rpw;  // rows of one launch: its x axis holds fewer than 2^32 threads
     for (a.row0 = 0; a.row0 < rows; a.row0 += run) {
         const int64_t n = rows - a.row0 < run ? rows - a.row0 : run;
-        hipLaunchKernelGGL((norm_kernel<W, PER, TPR>), dim3((unsigned)((n + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
+        hipLaunchKernelGGL((norm_kernel<W, PER, TPR, STREAM>), dim3((unsigned)((n + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
         if (hipError_t e = hipGetLastError()) return e;
     }
     return hipSuccess;
@@ -218,6 +222,14 @@ hipError_t launch_wide(const NormArgs &a, hipStream_t stream)
     if (chunks <= 32) return launch_as<W, 1, 32>(a, 256, stream);
     if (chunks <= 64) return launch_as<W, 1, 64>(a, 256, stream);
     if constexpr (W == 8) {
+        // Many rows: two chunks to a thread, so that half the waves wait at the exchange (8191 x 5120, bf16 onto bf16 into
+        // e4m3, 294 MB: 63 us against 72), and results of 8 and 16 bits past the caches (58); fp32 results that way are
+        // slower (sum in fp32, 461 MB: 93 against 87).
+        const bool many = (int64_t)a.n_tok * a.n_heads * a.d > (16 << 20);
+        if (many && chunks > 128 && chunks <= 1024) {
+            const bool f32 = (a.total.p && !a.total.bf16) || a.out_type == kF32;
+            return f32 ? launch_as<W, 2, 0>(a, threads(2), stream) : launch_as<W, 2, 0, true>(a, threads(2), stream);
+        }
         if (chunks <= 1024) return launch_as<W, 1, 0>(a, threads(1), stream);
         return launch_as<W, 2, 0>(a, threads(2), stream);  // d <= kNormMaxD = 2048 chunks of 8
     } else {
