@@ -8,6 +8,10 @@
 // otherwise (the sum over k does not depend on which k a lane holds, as long as x and w agree).  The product is taken
 // transposed (w's rows are MFMA's rows), so that a lane ends with quads of neighbouring columns of one row of out.  Of a gated
 // product a tile holds 16 gate rows beside the 16 up rows of the same columns, so that both are in the same lane.
+//
+// Few rows are bound by w's bytes (16 x 5120 -> 2 x 13824 e4m3: 29.5 us, 4.8 TB/s), many by the tiles' way from L2 beside the
+// matrix unit (1024 rows of the same 151 us, 1.92 PFLOP/s; 8191 x 5120 -> 12352 bf16 1.05 ms, 0.99; the library's products of
+// these sizes take 131 and 829 us).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -12,6 +12,10 @@
 // k-th largest of its threads' maxima, which one wave finds by halving; chunks that reach this bar go to a list in LDS, and
 // whenever that has grown its logits are ordered by counting, which leaves k of them and a higher bar.  Slices of one row
 // meet in the workspace, where a second kernel joins them.
+//
+// 1024 x 131071 bf16 with a token and 20 alternatives each: 67 us, 4.0 TB/s (a plain read 5.65); the vector unit issues for 79%
+// of the time: 8.5 instructions a logit (unpacking 1, the chunks' maxima 1.5, the exponent 1, the power 2, the sums 3).
+// One row of 131072: 6.7 us and 6.0 for the join.
 #include <algorithm>
 
 #include "gdn_rows.h"

