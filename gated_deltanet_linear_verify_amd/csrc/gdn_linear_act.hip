@@ -53,7 +53,7 @@ template <int T>
 constexpr int kElem = T == kBf16 ? 2 : 1;
 
 // 16 codes of e4m3 as bf16: the lower and the upper half.
-__device__ __forceinline__ void widen(i4 c, bf16x8_t &lo, bf16x8_t &hi)
+[[maybe_unused]] __device__ __forceinline__ void widen(i4 c, bf16x8_t &lo, bf16x8_t &hi)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
