@@ -2,9 +2,10 @@
 // alternatives (gfx950): what a verify step answers with (hf2q qwen35_target.rs, forward_decode_verify_batched: the
 // logits of every position and their argmax).
 //
-// In powers of two, with c = log2(e) / T and a whole number K next to c max x:  a = c x - K (one rounding: K is exact),
+// In powers of two, with c = log2(e) / T and a whole number K next to c max x:  a = c x - K (one rounding),
 // s = sum 2^a, u = sum 2^a a, and then lse = ln 2 (K + log2 s), entropy = ln 2 (log2 s - u / s) and the log probability of x
-// is ln 2 (a - log2 s).  c's own rounding is that of T, the same in all of them.
+// is ln 2 (a - log2 s).  c's own rounding is that of T, the same in all of them.  K is a whole number, but c max x was rounded
+// to fp32 on the way to it: the largest a is up to half a step of c max x from 0, 32 below 2^30, where kFar ends it.
 //
 // A workgroup runs over its slice of a row (the whole row where there are many) in batches of up to 32 KiB that it holds in
 // registers: every logit is read once, and a batch's maxima, sums, ranks and candidates come from there.  Each thread sums
@@ -71,9 +72,11 @@ __device__ __forceinline__ PartView part_at(const LogprobArgs &a, int64_t i)
             reinterpret_cast<uint64_t *>(p + sizeof(Part) + ((size_t)a.n_ids * 4 + 15) / 16 * 16)};
 }
 
-// Sums s and u against the exponent k.  A row (or slice) whose maximum is `far` has none: numbers of that size are equal or too
-// far apart for more than one of them to count (fp32's steps at 2^60 are 2^37), so s counts those that are equal to the top.
-constexpr float kFar = 0x1p60f, kNoExponent = -0x1p61f;
+// Sums s and u against the exponent k.  A row (or slice) whose maximum is `far` has none: from 2^30 on logits are equal or at
+// least 2^30 2^-24 = 64 powers of two apart, of which 2^24 together are 2^-40 of the largest, so s counts those that are
+// equal to the top.  Below, 2^a of the largest logit is within 2^33 of 1.  A thread whose logits are all below
+// kNoExponent keeps that exponent, and has nothing beside a row that is not far.
+constexpr float kFar = 0x1p30f, kNoExponent = -0x1p31f;
 __device__ __forceinline__ bool is_far(float top, float c) { return !(fabsf(top * c) < kFar); }
 struct Sums {
     float k, s, u;
