@@ -12,12 +12,11 @@
 // Few rows are bound by w's bytes (16 x 5120 -> 2 x 13824 e4m3: 29.5 us, 4.8 TB/s), many by the tiles' way from L2 beside the
 // matrix unit (1024 rows of the same 151 us, 1.92 PFLOP/s; 8191 x 5120 -> 12352 bf16 1.05 ms, 0.99; the library's products of
 // these sizes take 131 and 829 us).
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 
 #include "gdn_device.h"
 #include "gdn_internal.h"
+#include "gdn_tiles.h"
 
 namespace gdn {
 
@@ -28,7 +27,7 @@ typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i8v __attribute__((ext_vector_type(8)));
 
-constexpr int kRowBytes = 128, kChunks = kRowBytes / 16;
+constexpr int kRowBytes = kStepBytes, kChunks = kRowBytes / 16;
 
 __device__ __attribute__((aligned(16))) unsigned char kZeros[16];  // what a tile reads past the end of K
 
@@ -558,57 +557,6 @@ hipError_t launch_tile(const LinearActArgs &a, int wide, hipStream_t stream)
     return hipGetLastError();
 }
 
-// The tile shapes, as launch_of has them.
-enum Tile { kShort6, kShort4, k32x64, k64x64, k64x128, k128x128Deep, k128x128, k256x256 };
-struct Choice {
-    int tile, splits;
-};
-
-// A launch's tile and the parts of K, by what is expected of them.  Measured on products of 1 to 8191 rows, 5120 to 27648
-// columns and K of 4096 to 13824 in the three types, in us:
-// - Up to 64 rows the product is a stream of w.  The smallest tile that holds the rows spreads it over the most workgroups:
-//   16 rows by 64 columns (16 x 5120 -> 12352 bf16: 26.7, with 32 rows 30.3), 32 by 64 (32 rows: 30.6, with 32 by 128 43.5),
-//   64 by 64.  Six buffered tiles where workgroups are few (26.7 against 27.6 with four), four where there are more than 512
-//   (16 x 512 -> 65536: 16.7 against 20.1).  Below 160 tiles K is cut into parts of at least 16 steps (1 x 13824 -> 5120 e4m3:
-//   19 against 42; above, the join costs more than it gives: 193 tiles in two parts 32.4 against 26.7).
-// - Beyond that a tile's step takes about `step` us with one workgroup to a CU, and `more` for each further 256 tiles; the join
-//   reads what the parts write.  256 x 256 has the fewest bytes per flop and wins where its tiles fill whole rounds of
-//   256 CUs (1024 x 5120 -> 2 x 13824 e4m3, 432 tiles: 153 against 196 with 128 x 128), 128 x 128 two to a CU in between
-//   (4096 x 5120 -> 5120 bf16: 258 against 279), its three-buffer form where there is only one to a CU
-//   (256 x 5120 -> 12352: 63 against 85), 64 x 128 and 64 x 64 below; parts of K where even those leave CUs idle
-//   (1024 x 13824 -> 5120 i8, 80 tiles of 256 x 256: three parts 108, one 186; 128 x 128 in one part 125).
-Choice choose(int64_t M, int64_t N, int64_t K, int type, bool gated)
-{
-    const int64_t steps = (K * (type == kBf16 ? 2 : 1) + kRowBytes - 1) / kRowBytes, rows = gated ? 2 * N : N;
-    if (M <= 64) {
-        const int64_t tiles = (rows + 63) / 64;
-        const int64_t most = M <= 32 ? 240 : 480;  // workgroups that splitting aims at
-        const int splits = tiles >= 160 ? 1 : (int)std::max<int64_t>(1, std::min(steps / 16, (most + tiles - 1) / tiles));
-        return {M > 32 ? k64x64 : M > 16 ? k32x64 : tiles > 512 ? kShort4 : kShort6, splits};
-    }
-    struct {
-        int tile, bm, bn;
-        double step, more;
-        bool rounds;  // whole rounds of one workgroup to a CU
-    } const shapes[] = {{k256x256, 256, 256, 1.8, 1.8, true}, {k128x128, 128, 128, 1.0, 0.62, false}, {k128x128Deep, 128, 128, 0.7, 0.7, true},
-                        {k64x128, 64, 128, 0.5, 0.5, false}, {k64x64, 64, 64, 0.18, 0.4, false}};
-    Choice best{k256x256, 1};
-    double least = 1e30;
-    for (const auto &t : shapes)
-        for (int splits : {1, 2, 3, 4, 6, 8}) {
-            if (splits > 1 && steps / splits < 8) break;
-            const double tiles = (double)((M + t.bm - 1) / t.bm) * ((rows + t.bn - 1) / t.bn) * splits / 256;
-            const double at_once = t.rounds ? t.step * std::ceil(tiles) : std::max(t.step, t.more * tiles);
-            double us = at_once * (double)((steps + splits - 1) / splits);
-            if (splits > 1) us += 5 + (double)splits * M * rows * 8 / 4e6;
-            if (us < least) {
-                least = us;
-                best = {t.tile, splits};
-            }
-        }
-    return best;
-}
-
 template <int T, bool GATED>
 hipError_t launch_of(const LinearActArgs &a, int tile, int wide, hipStream_t stream)
 {
@@ -628,14 +576,14 @@ hipError_t launch_of(const LinearActArgs &a, int tile, int wide, hipStream_t str
 
 size_t linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int type, bool gated)
 {
-    const int splits = M ? choose(M, N, K, type, gated).splits : 1;
+    const int splits = M ? choose_tile(M, N, K, type == kBf16 ? 2 : 1, gated).splits : 1;
     return splits > 1 ? 16 * (size_t)splits * M * quads(N) * (gated ? 2 : 1) : 0;
 }
 
 hipError_t launch_linear_act(const LinearActArgs &args, hipStream_t stream)
 {
     LinearActArgs a = args;
-    const Choice c = choose(a.M, a.N, a.K, a.x.type, a.gated);
+    const Choice c = choose_tile(a.M, a.N, a.K, a.x.type == kBf16 ? 2 : 1, a.gated);
     a.splits = c.splits;
     const auto fits = [](const void *p, int64_t ld, int type) {
         return !p || ((uintptr_t)p % (type == kF32 ? 16 : 8) == 0 && ld % 4 == 0);
