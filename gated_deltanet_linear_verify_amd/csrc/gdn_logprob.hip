@@ -102,7 +102,7 @@ struct Row {
         far = is_far(top, c);
         logs = log2f(a.s);
         lse = far ? top * (c * kLn2) + logs * kLn2 : (k + logs) * kLn2;
-        entropy = far ? logs * kLn2 : (logs - a.u / a.s) * kLn2;
+        entropy = far ? logs * kLn2 : fmaxf(logs - a.u / a.s, 0.0f) * kLn2;  // of a row that is sure, both are a top's a
         if (empty) lse = -kInf, entropy = 0.0f;
         if (bad) lse = entropy = __builtin_nanf("");
     }

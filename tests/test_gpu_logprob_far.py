@@ -111,3 +111,13 @@ def test_temperatures(temperature, dtype):
             x[: v - 20] = fill
             rows.append(x)
         run(rows, dtype, n, temperature)
+
+
+def test_entropy_is_never_negative():
+    """Rows that are sure of a token: log s and u / s are equal up to their roundings."""
+    n, v = 4000, 300
+    x = torch.full((n, v), -60.0)
+    x[torch.arange(n), torch.arange(n) % v] = 37.0 * torch.rand(n, generator=torch.Generator().manual_seed(1))
+    for t in (1.0, 0.7, 3.0):
+        for rows in (x, x.to(torch.bfloat16)):
+            assert (call(rows.cuda(), temperature=t)["entropy"] >= 0).all()
