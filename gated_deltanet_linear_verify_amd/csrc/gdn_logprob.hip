@@ -111,7 +111,8 @@ struct Row {
         if (bad) return __builtin_nanf("");
         if (empty) return -kInf;
         const float d = __builtin_fmaf(x, c, -k);  // c x may pass fp32's range where ln 2 times it does not
-        if (far || (!(d > -kInf) && x > -kInf)) return (x - top) * (c * kLn2) - logs * kLn2;
+        // and x - top may where its halves, times 2 c, do not
+        if (far || (!(d > -kInf) && x > -kInf)) return (0.5f * x - 0.5f * top) * (2.0f * kLn2 * c) - logs * kLn2;
         return (d - logs) * kLn2;
     }
 };

@@ -121,3 +121,14 @@ def test_entropy_is_never_negative():
     for t in (1.0, 0.7, 3.0):
         for rows in (x, x.to(torch.bfloat16)):
             assert (call(rows.cuda(), temperature=t)["entropy"] >= 0).all()
+
+
+def test_log_probabilities_beside_a_maximum_of_the_other_sign():
+    """The difference of two logits passes fp32's range, and divided by T it does not."""
+    x = torch.zeros((3, 40))
+    x[0, 3], x[0, 5] = 3e38, -3e38
+    x[1, 3], x[1, 5] = 1e38, -3.3e38
+    x[2, 3], x[2, 5] = 3.4e38, -3.4e38
+    for t in (4.0, 1000.0):
+        run(list(x), "f32", 1, t)
+        run(list(x), "bf16", 1, t)
