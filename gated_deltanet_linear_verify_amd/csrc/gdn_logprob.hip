@@ -11,8 +11,11 @@
 // registers: every logit is read once, and a batch's maxima, sums, ranks and candidates come from there.  Each thread sums
 // against an exponent of its own, which rises with its maximum.  The k alternatives of the first batch are at least the
 // k-th largest of its threads' maxima, which one wave finds by halving; chunks that reach this bar go to a list in LDS, and
-// whenever that has grown its logits are ordered by counting, which leaves k of them and a higher bar.  Slices of one row
-// meet in the workspace, where a second kernel joins them.
+// whenever that has grown its logits are ordered by counting, which leaves k of them and a higher bar.  Where too many reach the
+// bar because they equal it (a finite mask over most of the row, a row of few values), only larger ones are listed, and the
+// places that those leave go to the equal ones by their index, in a pass behind the loop that ends with the last place (8 tokens of
+// 131072 allowed beside -1e10, top 20: 1024 rows 58 us, and 53 beside -infinity; one row 11 and 8, and 11 and 5 for the join; one
+// alternative at a time took 50 times as long).  Slices of one row meet in the workspace, where a second kernel joins them.
 //
 // 1024 x 131071 bf16 with a token and 20 alternatives each: 67 us, 4.0 TB/s (a plain read 5.65); the vector unit issues for 79%
 // of the time: 8.5 instructions a logit (unpacking 1, the chunks' maxima 1.5, the exponent 1, the power 2, the sums 3).
@@ -135,6 +138,21 @@ __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&x)[BF16 ?
     }
 }
 
+// What all threads read alike from LDS, in a scalar register.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
+
+// The thread's index as a value of its own: what a rare phase makes of it is computed there, not ahead of the loop around it,
+// where it would take registers all along.
+__device__ __forceinline__ int own_index()
+{
+    int t = threadIdx.x;
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(t));
+#endif
+    return t;
+}
+
 __device__ __forceinline__ float wave_max(float x)
 {
     x = fmaxf(x, dpp_mov<0xB1>(x));
@@ -177,6 +195,12 @@ __device__ __forceinline__ float below(float x)
     const uint32_t b = __float_as_uint(x);
     return __uint_as_float(x == 0.0f ? 0x80000001u : b & 0x80000000u ? b + 1 : b - 1);
 }
+// The smallest one above x, so that v > x where v >= above(x).
+__device__ __forceinline__ float above(float x)
+{
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float(x == 0.0f ? 1u : b & 0x80000000u ? b - 1 : b + 1);
+}
 
 // How many of the n keys are above `mine`, two to a read.
 __device__ __forceinline__ int count_above(const uint64_t *keys, int n, uint64_t mine)
@@ -195,7 +219,7 @@ __device__ __forceinline__ int count_above(const uint64_t *keys, int n, uint64_t
 template <bool BF16>
 __device__ void fill_masked(const LogprobArgs &a, int64_t row, const Row &r, int k)
 {
-    const int lane = threadIdx.x & 63;
+    const int lane = own_index() & 63;
     for (int i0 = 0; i0 < a.V && k < a.top_k; i0 += 64) {
         const int i = i0 + lane;
         const bool gone = i < a.V && fmaxf(logit<BF16>(a, row, i), -kInf) == -kInf;
@@ -214,12 +238,12 @@ template <bool BF16, int CH>
 __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs a, int slices)
 {
     constexpr int E = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4, kBatch = kThreads * CH;
-    __shared__ float tops[kThreads], sum_k[kWaves], sum_s[kWaves], sum_u[kWaves], given[kMaxIds], bar_lds;
+    __shared__ float tops[kThreads], singles[16], sum_k[kWaves], sum_s[kWaves], sum_u[kWaves], given[kMaxIds], bar_lds;
     __shared__ __attribute__((aligned(16))) uint4 hit[kHits];
     __shared__ __attribute__((aligned(16))) uint64_t list[2][kList];
     __shared__ uint64_t best[kWaves];
     __shared__ int hit_at[kHits], hits, listed, ids[kMaxIds], before[kMaxIds];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int64_t row = a.row0 + blockIdx.x / slices;
     const int slice = blockIdx.x % slices;
     // A row is `head` logits up to the first 16-byte boundary, chunks of 16 bytes, and a tail.  Head and tail go as single
@@ -232,10 +256,13 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
     const unsigned char *body = p + head * kSize;
     const float c2 = a.inv_t * kLog2E;
 
-    int extra = -1;
-    if (slice == 0 && tid < head) extra = tid;
-    if (slice == slices - 1 && tid >= 64 && tid < 64 + tail) extra = a.V - tail + tid - 64;
+    // They wait in LDS: kept in registers through the loop they would make others spill.
+    const bool in_head = slice == 0 && tid < head, in_tail = slice == slices - 1 && tid >= 64 && tid < 64 + tail;
+    auto extra_of = [&](int t) { return in_head ? t : in_tail ? a.V - tail + t - 64 : -1; };
+    auto single_of = [&](int t) -> float & { return singles[in_head ? t : 8 + (t & 7)]; };
+    const int extra = extra_of(tid);
     const float single = extra >= 0 ? logit<BF16>(a, row, extra) : -kInf;
+    if (extra >= 0) single_of(tid) = single;
     if (tid < a.n_ids) {
         int id = a.ids[row * a.n_ids + tid], n = 0;
         if (id < 0 || id >= a.V) id = -1;
@@ -251,31 +278,53 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
 
     Sums sum{kNoExponent, 0.0f, 0.0f};
     float top = fmaxf(single, -kInf), bar = -kInf;
-    int kept = 0;       // ordered entries at the front of list[side]
+    int kept = 0;        // ordered entries at the front of list[side]
     int side = 0;
-    bool slow = false;  // alternatives one at a time, behind the loop
+    bool first = true;   // nothing has been ordered yet
+    bool slow = false;   // alternatives one at a time, behind the loop
+    // Where very many logits are equal to the bar (a finite mask, a row of few values) only larger ones are listed: `equal` is
+    // that bar, which at least top_k logits of the slice reach, and the places that larger ones leave are filled behind the loop.
+    bool wide = false;   // at least top_k logits reach the bar, and those equal to it are listed
+    bool closed = false; // there is an `equal`
+    float equal = 0.0f;
+    auto close = [&] {
+        equal = bar;
+        bar = above(bar);
+        closed = true;
+        wide = false;
+    };
     auto add = [&](float x) {
         const float d = __builtin_fmaf(x, c2, -sum.k), e = __builtin_amdgcn_exp2f(d);
         sum.s += e;
         sum.u = __builtin_fmaf(e, fmaxf(d, -1e30f), sum.u);  // a masked logit's e is 0, but not its d
     };
     // The logits of the listed chunks that reach the bar, and what was kept, ordered: all threads, between barriers.
-    // Those of -infinity are not listed.
+    // Those of -infinity are not listed.  The head's come first, as its indexes do, and the tail's last.
     auto order = [&](int n_hits, bool last) {
+        const int tid = own_index();
         auto offer = [&](float x, int i) {
             if (x >= bar && x > -kInf) {
                 const int at = kept + atomicAdd(&listed, 1);
                 if (at < kList) list[side][at] = key_of(x, i);
             }
         };
-        for (int i = tid; i < n_hits * E; i += kThreads) {
-            const int c = i / E, j = i % E;
-            const uint32_t v = reinterpret_cast<const uint32_t *>(hit)[4 * c + (BF16 ? j / 2 : j)];
-            offer(__uint_as_float(BF16 ? (j % 2 ? v & 0xffff0000u : v << 16) : v), hit_at[c] * E + j + head);
+        int n;
+        for (;;) {
+            for (int i = tid; i < n_hits * E; i += kThreads) {
+                const int c = i / E, j = i % E;
+                const uint32_t v = reinterpret_cast<const uint32_t *>(hit)[4 * c + (BF16 ? j / 2 : j)];
+                offer(__uint_as_float(BF16 ? (j % 2 ? v & 0xffff0000u : v << 16) : v), hit_at[c] * E + j + head);
+            }
+            if ((in_head && first) || (in_tail && last)) offer(single_of(tid), extra_of(tid));
+            __syncthreads();
+            n = kept + uniform(listed);
+            if (n <= kList || !wide) break;
+            close();
+            __syncthreads();
+            if (tid == 0) listed = 0;
+            __syncthreads();
         }
-        if (last && extra >= 0) offer(single, extra);
-        __syncthreads();
-        const int n = kept + listed;
+        first = false;
         if (n > kList) {
             slow = true;
         } else {
@@ -289,21 +338,33 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
             side ^= 1;
         }
         __syncthreads();
-        if (kept == a.top_k && !slow) bar = fmaxf(bar, bar_lds);
+        // those that come behind and equal the last one kept are after it
+        const float last_kept = uniform(bar_lds);
+        if (kept == a.top_k && !slow && last_kept >= bar) {
+            bar = above(last_kept);
+            wide = false;
+        }
         if (tid == 0) hits = listed = 0;
         __syncthreads();
     };
 
     uint32_t w[CH][4];
-    auto load = [&](int b, int i) {  // chunk i of the batch from b on
+    auto load_at = [&](int c, uint32_t (&to)[4]) {  // chunk c, of -infinities past the slice's end
         uint4 v = make_uint4(kNone<BF16>, kNone<BF16>, kNone<BF16>, kNone<BF16>);
-        const int c = b + tid + i * kThreads;
         if (c < c1) v = *reinterpret_cast<const uint4 *>(body + (uint32_t)c * 16u);
-        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+        to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
     };
+    auto load = [&](int b, int i) { load_at(b + tid + i * kThreads, w[i]); };  // chunk i of the batch from b on
 #pragma unroll
     for (int i = 0; i < CH; ++i) load(c0, i);
+    sum.k = fmaxf(sum.k, rintf(single * c2));
+    add(single);
     __syncthreads();
+    if (extra >= 0)
+        for (int k = 0; k < a.n_ids; ++k) {
+            const float mine = fmaxf(given[k], -kInf);
+            if (!(single <= (extra < ids[k] ? below(mine) : mine))) atomicAdd(&before[k], 1);
+        }
 #pragma unroll 1
     for (int b0 = c0; b0 < c1 || b0 == c0; b0 += kBatch) {
         float cm[CH], batch_top = b0 == c0 ? top : -kInf;  // the largest of each chunk, and of the thread's
@@ -320,7 +381,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
             const float mine = fmaxf(given[k], -kInf);
             if (id < 0 || !__ballot(batch_top >= mine)) continue;
             const float or_equal = below(mine);
-            int n = b0 == c0 ? __popcll(__ballot(extra >= 0 && !(single <= (extra < id ? or_equal : mine)))) : 0;
+            int n = 0;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 if (!__ballot(cm[i] >= mine)) continue;
@@ -334,8 +395,10 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
             }
             if (lane == 0) atomicAdd(&before[k], n);
         }
-        for (bool again = false; a.top_k && !slow; again = true) {
-            if (b0 == c0 || again) {
+        float raised = -kInf;
+        // stage 1 raises the bar by this batch's maxima, stage 2 leaves what equals it for later
+        for (int stage = b0 == c0; a.top_k && !slow; ++stage) {
+            if (stage == 1) {
                 // a bar that at least top_k of the threads' maxima reach, and few more: by halving the range that they span
                 tops[tid] = batch_top;
                 __syncthreads();
@@ -368,9 +431,18 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
                     if (lane == 0) bar_lds = value_of(found);
                 }
                 __syncthreads();
-                bar = fmaxf(bar, bar_lds);
+                const float most = uniform(bar_lds);
+                if (most >= bar) {
+                    bar = most;
+                    wide = bar > -kInf;
+                }
+                raised = bar;
+            } else if (stage > 1) {
+                if (stage > 2 || (bar == raised && !wide)) slow = true;
+                if (slow) break;
+                if (bar == raised) close();
             }
-            const int had = hits;
+            const int had = uniform(hits);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -383,18 +455,14 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
                 }
             }
             __syncthreads();
-            const int have = hits;
-            if (have <= kHits && (b0 == c0 || again || have - had <= kMany)) {
-                if (have > kMany) order(have, false);
-                break;
-            }
-            // logits that rise from batch to batch, or the first that are not masked: order what was there before, and raise
-            // the bar by this batch's maxima
-            if (again) slow = true;
-            order(had, false);
+            const int have = uniform(hits);
+            // too many: logits that rise from batch to batch, the first that are not masked, or very many equal ones; what was there
+            // before is ordered, and the bar raised
+            const bool fit = have <= kHits && (stage || have - had <= kMany);
+            if (!fit || have > kMany) order(fit ? have : had, false);
+            if (fit) break;
         }
         // the sums, each chunk's registers taking the next batch's at once
-        if (b0 == c0) add(single);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             if (b0 + i * kThreads >= c1) continue;
@@ -406,6 +474,9 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
         }
     }
 
+    tid = own_index();
+    wave = tid >> 6;
+    lane = tid & 63;
     // the workgroup's maximum and sums
     {
         float k = wave_max(sum.k), t = wave_max(fmaxf(top, -kInf));
@@ -438,7 +509,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
         float n = 0.0f;
         auto count = [&](float x) { n += !(x < kInf) ? __builtin_nanf("") : x == top ? 1.0f : 0.0f; };
         for (int i = first_i + tid; i < end_i; i += kThreads) count(logit<BF16>(a, row, i));
-        if (extra >= 0) count(single);
+        if (extra_of(tid) >= 0) count(single_of(tid));
         n = wave_sum(n);
         __syncthreads();
         if (lane == 0) sum_s[wave] = n;
@@ -456,7 +527,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
         for (int k = 0; k < a.n_ids; ++k) {
             if (ids[k] < 0) continue;
             const uint64_t key = key_of(given[k], ids[k]);
-            int n = extra >= 0 && key_of(single, extra) > key;
+            int n = extra_of(tid) >= 0 && key_of(single_of(tid), extra_of(tid)) > key;
             for (int i = first_i + tid; i < end_i; i += kThreads) n += key_of(logit<BF16>(a, row, i), i) > key;
             if (n) atomicAdd(&before[k], n);
         }
@@ -485,14 +556,50 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
     };
     if (!slow && !r.bad) order(hits, true);
     if (!slow && !r.bad) {
-        for (int i = tid; i < (whole ? kept : a.top_k); i += kThreads) put(i, i < kept ? list[side][i] : 0);
-        if (whole && kept < a.top_k && wave == 0) fill_masked<BF16>(a, row, r, kept);
+        int n = kept;
+        if (closed) n = __popcll(__ballot(lane < kept && (uint32_t)(list[side][lane] >> 32) > order_of(equal)));
+        for (int i = tid; i < (whole || closed ? n : a.top_k); i += kThreads) put(i, i < n ? list[side][i] : 0);
+        if (!closed) {
+            if (whole && n < a.top_k && wave == 0) fill_masked<BF16>(a, row, r, n);
+            return;
+        }
+        // places n .. top_k: those equal to `equal` by their index, up to a chunk per thread at a time (bit j: base + j is one)
+        auto fill = [&](uint32_t which, int base) {
+            int upto = __popc(which);
+#pragma unroll
+            for (int o = 1; o < 64; o *= 2) {
+                const int u = __shfl_up(upto, o);
+                upto += lane >= o ? u : 0;
+            }
+            __syncthreads();  // the last round's counts have been read
+            if (lane == 63) hit_at[wave] = upto;
+            __syncthreads();
+            int at = n + upto - __popc(which);
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                at += i < wave ? hit_at[i] : 0;
+                n += hit_at[i];
+            }
+            for (; which && at < a.top_k; which &= which - 1) put(at++, key_of(equal, base + __ffs(which) - 1));
+        };
+        if (n < a.top_k) fill(in_head && single_of(tid) == equal, tid);
+        for (int b = c0; b < c1 && n < a.top_k; b += kThreads) {
+            load_at(b + tid, w[0]);
+            float x[E];
+            unpack<BF16>(w[0], x);
+            uint32_t which = 0;
+#pragma unroll
+            for (int j = 0; j < E; ++j) which |= (uint32_t)(x[j] == equal) << j;
+            fill(which, (b + tid) * E + head);
+        }
+        if (n < a.top_k) fill(in_tail && single_of(tid) == equal, extra_of(tid));
         return;
     }
-    // Very many equal logits, or a NaN or +infinity among them: one alternative at a time, the largest key below the last.
+    // A NaN or +infinity among the logits, or candidates past the lists, as where few threads hold them all: one alternative at a
+    // time, the largest key below the last.
     uint64_t last = ~0ull;
     for (int k = 0; k < a.top_k; ++k) {
-        uint64_t mine = extra >= 0 ? key_of(single, extra) : 0;
+        uint64_t mine = extra_of(tid) >= 0 ? key_of(single_of(tid), extra_of(tid)) : 0;
         if (mine >= last) mine = 0;
         for (int i = first_i + tid; i < end_i; i += kThreads) {
             const uint64_t key = key_of(logit<BF16>(a, row, i), i);
@@ -581,22 +688,29 @@ __global__ __launch_bounds__(kThreads) void logprob_join_kernel(LogprobArgs a, i
         a.top_logprob[row * a.top_k + k] = r.lp(x);
     };
     // The slices' keys are in order: the top_k-th of the first few of each is a bar that at least top_k keys reach, and not
-    // many more (counting among all of them took 30 us for 32 slices of 20, this 4).
-    const int n = slices * a.top_k, each = (a.top_k + slices - 1) / slices, m = each * slices;
+    // many more (counting among all of them took 30 us for 32 slices of 20, this 4).  Where many logits are equal, the first
+    // slices have all the keys, and a bar from as many of each as there are threads leaves fewer of them.
+    const int n = slices * a.top_k;
     uint64_t *some = keys + (n + 1) / 2 * 2;
-    if (tid < m) some[tid] = keys[tid / each * a.top_k + tid % each];
-    __syncthreads();
-    if (tid < m && some[tid] && count_above(some, m, some[tid]) == a.top_k - 1) bar = some[tid];
-    __syncthreads();
-    int mine = 0;
-    for (int i = tid; i < n; i += kThreads) {
-        const uint64_t key = keys[i];
-        if (!key || value_of((uint32_t)(key >> 32)) == -kInf) continue;
-        ++mine;
-        if (key >= bar) some[atomicAdd(&listed, 1)] = key;
+    for (int each = (a.top_k + slices - 1) / slices, last = 0;; each = min(a.top_k, kThreads / slices), last = 1) {
+        const int m = each * slices;
+        if (tid < m) some[tid] = keys[tid / each * a.top_k + tid % each];
+        __syncthreads();
+        if (tid < m && some[tid] && count_above(some, m, some[tid]) == a.top_k - 1) bar = some[tid];
+        __syncthreads();
+        int mine = 0;
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t key = keys[i];
+            if (!key || value_of((uint32_t)(key >> 32)) == -kInf) continue;
+            ++mine;
+            if (key >= bar) some[atomicAdd(&listed, 1)] = key;
+        }
+        if (mine && !last) atomicAdd(&found, mine);
+        __syncthreads();
+        if (last || listed <= kThreads / 2) break;
+        __syncthreads();
+        if (tid == 0) listed = 0;
     }
-    if (mine) atomicAdd(&found, mine);
-    __syncthreads();
     for (int i = tid; i < listed; i += kThreads) {
         const uint64_t key = some[i];
         const int place = count_above(some, listed, key);

@@ -664,7 +664,9 @@ size_t gdn_linear_act_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t d
  * Logits of -infinity (masked tokens) have probability 0 and add nothing; a row of nothing else has lse and log
  * probabilities -infinity and entropy 0.  A row that holds a NaN or +infinity has NaN for lse, entropy and the log
  * probabilities of valid tokens.  Every output is optional (NULL); logprob and rank need ids, and top_ids and top_logprob come together.
- * Sums are in fp32; every logit is read once, beside those of the given tokens.
+ * Sums are in fp32.  Every logit is read once, beside those of the given tokens; up to twice where very many are equal to
+ * one of the alternatives (a finite mask over most of a row) or where log2(e) / T times the largest is beyond 2^30, and in a row
+ * with a NaN or +infinity once more for each given token and each alternative.
  *   logits: aligned to their elements, any row stride.  n_rows 0 .. 2^26 (0 is a no-op); n_vocab 1 .. 2^24;
  *   n_ids 0 .. 64; top_k 0 .. min(64, n_vocab); temperature: from 2^-20 to 2^20.
  *   workspace: as gdn_linear_act's, of gdn_logprob_workspace_bytes.
