@@ -135,11 +135,13 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
     if (a.rms) {
         const float n = (float)d;
         r = 1.0f / sqrtf(ssq / n + a.eps);
-        if (!(ssq < __builtin_inff())) {  // the same for all lanes of a row
+        if (!(ssq < __builtin_inff()) || top >= 0x7f800000u) {  // the same for all lanes of a row
             uint32_t big;
             measure(ssq, big, false);
-            if (big < 0x7f800000u) {  // finite values: scaled by the power of two that puts the largest in [1, 2)
-                const int e = (int)(big >> 23) - 127;
+            // finite values, some of them above 1: scaled by the power of two that puts the largest in [1/2, 1), where neither
+            // their squares nor their products with any weight pass fp32's range
+            if (big < 0x7f800000u && big >= 0x3f800000u) {
+                const int e = (int)(big >> 23) - 126;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
 #pragma unroll

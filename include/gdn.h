@@ -594,7 +594,8 @@ size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n_batch, 
  *   nearest, ties to even
  * mode GDN_NORM_NONE leaves the division out: y = s * weight (what a caller wants that only adds or rounds to 8 bits).
  * Sums are in fp32 and y is formed from the s before its rounding; total and out are each rounded once.  Rows whose
- * squares pass fp32's range are scaled first, so that every finite row has its norm.  A row of zeros, or of values so
+ * squares or products s * weight pass fp32's range are scaled first, so that every finite row has its norm; products below
+ * 2^-126 keep fewer bits.  A row of zeros, or of values so
  * small that 1 / scale overflows, has codes and scale 0; a row of y that holds an infinity or a NaN gets codes 0 and
  * scale NaN, as in gdn_kv_write.
  *   x, residual, total: rows of equal n_heads (1 .. 8192), GDN_F32 or GDN_BF16, aligned to their elements; a token's
