@@ -214,7 +214,7 @@ hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
 
 // ---- norms, products with an epilogue, log probabilities ----
 enum { kF32 = 0, kBf16 = 1, kE4m3 = 2, kI8 = 3 };  // gdn_dtype
-constexpr int kNormMaxD = 16384;
+constexpr int kNormMaxD = 16384, kNormMaxLong = 65536;  // with the norm's division, and without
 struct NormArgs {
     RowsView x, residual, total, out;  // residual.p, total.p NULL: none; out.bf16 counts for out_type F32 and BF16 only
     const float *weight;               // or NULL

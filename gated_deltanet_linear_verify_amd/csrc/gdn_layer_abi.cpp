@@ -83,7 +83,8 @@ GDN_API int gdn_norm(const gdn_rows *x, const gdn_rows *residual, const gdn_rows
     if (!x || !out) return abi_fail(GDN_ERR_ARG, "%s: x and out must not be NULL", fn);
     if (mode != GDN_NORM_RMS && mode != GDN_NORM_NONE) return abi_fail(GDN_ERR_ARG, "%s: unknown mode %d", fn, mode);
     if (n_tok < 0) return abi_fail(GDN_ERR_RANGE, "%s: n_tok %d is negative", fn, n_tok);
-    if (d < 1 || d > kNormMaxD) return abi_fail(GDN_ERR_SHAPE, "%s: d must be 1 .. %d (got %d)", fn, kNormMaxD, d);
+    const int most = mode == GDN_NORM_NONE ? kNormMaxLong : kNormMaxD;
+    if (d < 1 || d > most) return abi_fail(GDN_ERR_SHAPE, "%s: d must be 1 .. %d in this mode (got %d)", fn, most, d);
     if (x->n_heads < 1 || x->n_heads > 8192) return abi_fail(GDN_ERR_SHAPE, "%s: n_heads must be 1 .. 8192", fn);
     if ((int64_t)n_tok * x->n_heads > kMaxTokenRows) return abi_fail(GDN_ERR_SHAPE, "%s: more than 2^26 rows", fn);
     if (mode == GDN_NORM_RMS && (!(eps >= 0x1p-126f) || !std::isfinite(eps)))

@@ -36,13 +36,51 @@ __device__ __forceinline__ void lanes_reduce(float &a, uint32_t &b)
     }
 }
 
+// What brings a row to 8 bits, from its largest size.
+struct Scale {
+    float scale, inv;
+    bool finite;  // neither infinite nor NaN
+    __device__ Scale(float most, int type) : scale(most / (type == kE4m3 ? 448.0f : 127.0f)), inv(1.0f / scale), finite(most < __builtin_inff())
+    {
+        if (!(inv < __builtin_inff())) scale = inv = 0.0f;  // a row of zeros, or of values whose 1 / scale overflows
+        if (!finite) {
+            scale = __builtin_nanf("");
+            inv = 0.0f;
+        }
+    }
+};
+
+// The codes of W neighbouring values y.
+template <int W, bool STREAM>
+__device__ __forceinline__ void store_codes(unsigned char *to, int type, const Scale &q, const float (&y)[W])
+{
+#pragma clang fp contract(off)  // a code is the rounded y (1 / scale)
+    uint32_t code[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const float z = q.finite ? y[j] * q.inv : 0.0f;
+        if (type == kE4m3)
+            code[j] = __builtin_amdgcn_cvt_pk_fp8_f32(z, 0.0f, 0, false) & 0xff;
+        else  // |z| <= 127 (1 + 2^-22): adding 1.5 2^23 rounds to nearest, ties to even
+            code[j] = __float_as_uint(z + 12582912.0f) & 0xff;
+    }
+    if constexpr (W == 8) {
+        const uint32_t lo = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+        const uint32_t hi = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+        put_row<STREAM>(reinterpret_cast<uint64_t *>(to), lo | (uint64_t)hi << 32);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) to[j] = (unsigned char)code[j];
+    }
+}
+
 // W channels per chunk (8 where every row is aligned for it, else 1), PER chunks per thread.  TPR > 0: a row is TPR
 // neighbouring lanes of a wave, 256 / TPR rows to a workgroup; TPR == 0: a row is a workgroup.  STREAM: results of 8 and
 // 16 bits past the caches.
 template <int W, int PER, int TPR, bool STREAM>
 __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
 {
-#pragma clang fp contract(off)  // y is the rounded product (s w) r, a code the rounded y (1 / scale)
+#pragma clang fp contract(off)  // y is the rounded product (s w) r
     __shared__ float sums[16];
     __shared__ uint32_t tops[16];
     const int rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
@@ -162,55 +200,90 @@ __global__ __launch_bounds__(TPR ? 256 : 1024) void norm_kernel(NormArgs a)
         }
         return;
     }
-    const float most = __uint_as_float(top) * r, full = a.out_type == kE4m3 ? 448.0f : 127.0f;
-    const bool finite = most < __builtin_inff();  // neither infinite nor NaN
-    float scale = most / full, inv = 1.0f / scale;
-    if (!(inv < __builtin_inff())) scale = inv = 0.0f;  // a row of zeros, or of values whose 1 / scale overflows
-    if (!finite) {
-        scale = __builtin_nanf("");
-        inv = 0.0f;
-    }
+    const Scale q(__uint_as_float(top) * r, a.out_type);
     unsigned char *to = static_cast<unsigned char *>(a.out.p) + oat;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int c = (li + i * tpr) * W;
         if (c >= d || !live) continue;
-        uint32_t code[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const float y = finite ? v[i][j] * w[i][j] * r * inv : 0.0f;
-            if (a.out_type == kE4m3)
-                code[j] = __builtin_amdgcn_cvt_pk_fp8_f32(y, 0.0f, 0, false) & 0xff;
-            else  // |y| <= 127 (1 + 2^-22): adding 1.5 2^23 rounds to nearest, ties to even
-                code[j] = __float_as_uint(y + 12582912.0f) & 0xff;
-        }
-        if constexpr (W == 8) {
-            const uint32_t lo = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-            const uint32_t hi = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-            const uint64_t codes8 = lo | (uint64_t)hi << 32;
-            if constexpr (STREAM)
-                __builtin_nontemporal_store(codes8, reinterpret_cast<uint64_t *>(to + c));
-            else
-                *reinterpret_cast<uint64_t *>(to + c) = codes8;
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) to[c + j] = (unsigned char)code[j];
-        }
+        for (int j = 0; j < W; ++j) v[i][j] = v[i][j] * w[i][j] * r;
+        store_codes<W, STREAM>(to + c, a.out_type, q, v[i]);
     }
-    if (li == 0 && live) a.scale[row] = scale;
+    if (li == 0 && live) a.scale[row] = q.scale;
 }
 
-template <int W, int PER, int TPR, bool STREAM = false>
-hipError_t launch_as(NormArgs a, int threads, hipStream_t stream)
+// Rows past kNormMaxD, without the division: a workgroup reads its row for the largest |s w| where codes ask for it, and
+// again, out of the caches, for the results.  A thread reads what it writes, so both may be in place.  (8-bit operands as wide as
+// an FFN's inner rows: 1024 x 25600 bf16 into e4m3 34 us, 79 MB read and written, and 52 MB of it read again; 16 x 17408 9 us.)
+constexpr int kLongThreads = 1024;
+template <int W>
+__global__ __launch_bounds__(kLongThreads) void long_rows_kernel(NormArgs a)
 {
-    const int64_t rows = (int64_t)a.n_tok * a.n_heads, rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
-    const int64_t run = (int64_t)0xffffffff / threads * rpw;  // rows of one launch: its x axis holds fewer than 2^32 threads
+    __shared__ uint32_t tops[kLongThreads / 64];
+    const int tid = threadIdx.x;
+    const int64_t row = a.row0 + blockIdx.x, t = row / a.n_heads, h = row % a.n_heads;
+    const int64_t xat = t * a.x.ld + h * a.x.hd, rat = t * a.residual.ld + h * a.residual.hd;
+    auto read = [&](int c, float (&s)[W], float (&y)[W]) {
+        float u[W], w[W];
+        load_row<W>(a.x.p, xat + c, a.x.bf16, s);
+        if (a.residual.p) load_row<W>(a.residual.p, rat + c, a.residual.bf16, u);
+        if (a.weight) load_row<W>(a.weight, c, false, w);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            if (a.residual.p) s[j] += u[j];
+            y[j] = a.weight ? s[j] * w[j] : s[j];
+        }
+    };
+    const bool codes = a.out_type == kE4m3 || a.out_type == kI8;
+    uint32_t top = 0;
+    if (codes) {
+        for (int c = tid * W; c < a.d; c += kLongThreads * W) {
+            float s[W], y[W];
+            read(c, s, y);
+#pragma unroll
+            for (int j = 0; j < W; ++j) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
+        }
+        float none = 0.0f;
+        lanes_reduce<64>(none, top);
+        if ((tid & 63) == 0) tops[tid >> 6] = top;
+        __syncthreads();
+        top = tops[tid & 15];
+        lanes_reduce<16>(none, top);
+    }
+    const Scale q(__uint_as_float(top), a.out_type);
+    const int64_t tat = t * a.total.ld + h * a.total.hd, oat = t * a.out.ld + h * a.out.hd;
+    for (int c = tid * W; c < a.d; c += kLongThreads * W) {
+        float s[W], y[W];
+        read(c, s, y);
+        if (a.total.p) store_row<W>(a.total.p, tat + c, a.total.bf16, s);
+        if (codes)
+            store_codes<W, false>(static_cast<unsigned char *>(a.out.p) + oat + c, a.out_type, q, y);
+        else
+            store_row<W>(a.out.p, oat + c, a.out.bf16, y);
+    }
+    if (codes && tid == 0) a.scale[row] = q.scale;
+}
+
+// launch(n, a) for runs of n rows from a.row0 on: a launch's x axis holds fewer than 2^32 threads.
+template <class F>
+hipError_t in_runs(NormArgs a, int64_t run, F launch)
+{
+    const int64_t rows = (int64_t)a.n_tok * a.n_heads;
     for (a.row0 = 0; a.row0 < rows; a.row0 += run) {
-        const int64_t n = rows - a.row0 < run ? rows - a.row0 : run;
-        hipLaunchKernelGGL((norm_kernel<W, PER, TPR, STREAM>), dim3((unsigned)((n + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
+        launch(rows - a.row0 < run ? rows - a.row0 : run, a);
         if (hipError_t e = hipGetLastError()) return e;
     }
     return hipSuccess;
+}
+
+template <int W, int PER, int TPR, bool STREAM = false>
+hipError_t launch_as(const NormArgs &args, int threads, hipStream_t stream)
+{
+    const int64_t rpw = TPR ? 256 / (TPR ? TPR : 1) : 1;
+    return in_runs(args, (int64_t)0xffffffff / threads * rpw, [&](int64_t n, const NormArgs &a) {
+        hipLaunchKernelGGL((norm_kernel<W, PER, TPR, STREAM>), dim3((unsigned)((n + rpw - 1) / rpw)), dim3(threads), 0, stream, a);
+    });
 }
 
 // A row's threads: neighbouring lanes of a wave up to 64 chunks (single channels: up to 512, eight to a lane, as a load
@@ -220,6 +293,10 @@ hipError_t launch_as(NormArgs a, int threads, hipStream_t stream)
 template <int W>
 hipError_t launch_wide(const NormArgs &a, hipStream_t stream)
 {
+    if (a.d > kNormMaxD)
+        return in_runs(a, 0xffffffff / kLongThreads, [&](int64_t n, const NormArgs &b) {
+            hipLaunchKernelGGL((long_rows_kernel<W>), dim3((unsigned)n), dim3(kLongThreads), 0, stream, b);
+        });
     const int chunks = (a.d + W - 1) / W;
     const auto threads = [&](int per) { return ((chunks + per - 1) / per + 63) / 64 * 64; };
     if (chunks <= 8) return launch_as<W, 1, 8>(a, 256, stream);

@@ -224,7 +224,8 @@ CODES = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "i8": torch.int8}
 
 
 def quantise_rows(x, fmt: str, out=None, scale=None, stream=None) -> tuple:
-    """(codes [rows][K], scales [rows]) of a bf16 or fp32 matrix x in ``fmt`` (e4m3 or i8); (x, None) for bf16."""
+    """(codes [rows][K], scales [rows]) of a bf16 or fp32 matrix x in ``fmt`` (e4m3 or i8; K up to 65536); (x, None) for
+    bf16."""
     if fmt == "bf16":
         return x, None
     rows, K = x.shape

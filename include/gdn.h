@@ -602,7 +602,7 @@ size_t gdn_attn_workspace_bytes(const gdn_kv *kv, int32_t n_q, int32_t n_batch, 
  *   heads may lie inside wider rows.  out: also GDN_E4M3 and GDN_I8; scale: fp32 [n_tok][n_heads], given for those
  *   types only.  total and out may each be x or residual in place, with the same strides and type, but not both the same
  *   one.  Otherwise what is written must not overlap anything else of the call.
- *   d 1 .. 16384; n_tok >= 0 (0 is a no-op), n_tok * n_heads <= 2^26; eps >= 2^-126 and finite.
+ *   d 1 .. 16384, with GDN_NORM_NONE 1 .. 65536; n_tok >= 0 (0 is a no-op), n_tok * n_heads <= 2^26; eps >= 2^-126 and finite.
  * Errors: NULL x or out, a scale that is missing or given for the wrong type, a pointer that is not aligned to its
  * elements, the same pointer with other strides or types, rows to write that overlap themselves, bad eps or mode ->
  * GDN_ERR_ARG; d, n_heads, too many rows -> GDN_ERR_SHAPE; n_tok < 0 -> GDN_ERR_RANGE; dtype -> GDN_ERR_DTYPE.
