@@ -177,7 +177,7 @@ def block_step(d: dict, stream=None) -> None:
 
 
 def upload_attention(inp: dict, rope: "gdn.gdn_rope_table", *, fmt: int, page_size: int, n_pages: int,
-                     prefix: bool = False, q_norm=None, k_norm=None) -> dict:
+                     prefix: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6) -> dict:
     """Device tensors of one attention_step (workloads.make_attention_inputs): x [B*T][hidden], the
     concatenated weight w_in [(n_q + 2 n_kv) d][hidden], the fused rows qkv [B*T][n_q + 2 n_kv][d] with the
     views q, k and v of them, w_out, y, an empty cache of n_pages pages and the workspace.  The round's lists
@@ -197,6 +197,7 @@ def upload_attention(inp: dict, rope: "gdn.gdn_rope_table", *, fmt: int, page_si
     sc = [torch.zeros((n_pages, n_kv, page_size), dtype=torch.float32, device="cuda") for _ in range(2 if fmt else 0)]
     d["kv"] = gdn.KvCache(k, v, *sc)
     d["workspace"] = torch.empty(gdn.gdn_attn_workspace_bytes(d["kv"], n_q, B, T, prefix), dtype=torch.uint8, device="cuda")
+    d["eps"] = eps  # of those norms (struct TargetWeights: rms_eps)
     for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):  # weights [d] of the heads' norms, where the layer has them
         d[name] = None if w is None else torch.from_numpy(np.ascontiguousarray(w, dtype=np.float32)).cuda()
     return d
@@ -212,7 +213,7 @@ def attention_step(d: dict, table, start, positions, n_new=None, parent=None, pr
     gdn.gdn_linear(d["x"], d["w_in"], M, N, d["hidden"], [(0, N, d["qkv"], N, 0)], stream)
     for name in ("q", "k"):
         if d.get(name + "_norm") is not None:
-            gdn.gdn_norm(d[name], d[name + "_norm"], d[name], M, stream=stream)
+            gdn.gdn_norm(d[name], d[name + "_norm"], d[name], M, eps=d.get("eps", 1e-6), stream=stream)
     gdn.gdn_rope(d["rope"], [(d["q"], d["q"])], positions, M, stream=stream)
     gdn.gdn_kv_write(kv, d["k"], d["v"], table, start, n_new, B, T, rope=d["rope"], positions=positions, stream=stream)
     gdn.gdn_attn_verify(kv, d["q"], table, start, n_new, parent, prefix_pages, prefix_len, d["out"], B, T, d["scale"],
@@ -241,15 +242,15 @@ def _scratch_bytes(M: int, fmt: str, *sizes) -> int:
     return max([16] + [gdn.gdn_linear_act_workspace_bytes(M, N, K, CODES[fmt], gated) for N, K, gated in sizes])
 
 
-def upload_ffn(inp: dict, *, fmt: str = "bf16") -> dict:
+def upload_ffn(inp: dict, *, fmt: str = "bf16", eps: float = 1e-6) -> dict:
     """Device tensors of one ffn_step (workloads.make_ffn_inputs): x [M][hidden] bf16 (the mixer's output), stream
-    [M][hidden] fp32 (the residual stream), norm_w, the weights gate_up [2 width][hidden] and down [hidden][width] in
-    ``fmt`` (bf16, e4m3 or i8, the 8-bit ones with a scale per row), the buffers between them and the workspace."""
+    [M][hidden] fp32 (the residual stream), norm_w and the norm's eps, the weights gate_up [2 width][hidden] and down
+    [hidden][width] in ``fmt`` (bf16, e4m3 or i8, the 8-bit ones with a scale per row), the buffers between them and the workspace."""
     f32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda()
     M, hidden = inp["x"].shape
     width = inp["w_down"].shape[1]
     d = {"M": M, "hidden": hidden, "width": width, "fmt": fmt, "x": f32(inp["x"]).bfloat16(), "stream": f32(inp["stream"]),
-         "norm_w": f32(inp["norm_w"])}
+         "norm_w": f32(inp["norm_w"]), "eps": eps}
     for n in ("gate_up", "down"):
         d["w_" + n], d[n + "_scale"] = quantise_rows(f32(inp["w_" + n]).bfloat16(), fmt)
     new = lambda K: torch.empty((M, K), dtype=torch.uint8 if fmt != "bf16" else torch.bfloat16, device="cuda").view(CODES[fmt])
@@ -269,7 +270,7 @@ def ffn_step(d: dict, stream=None) -> None:
     M, K, F, ws = d["M"], d["hidden"], d["width"], d["workspace"]
     rows = lambda t: None if t is None else t[:, None]
     gdn.gdn_norm(rows(d["x"]), d["norm_w"], rows(d["h"]), M, residual=rows(d["stream"]), total=rows(d["stream"]),
-                 scale=rows(d["h_scale"]), stream=stream)
+                 scale=rows(d["h_scale"]), eps=d.get("eps", 1e-6), stream=stream)
     gdn.gdn_linear_act(d["h"], d["w_gate_up"], d["act"], M, F, K, x_scale=d["h_scale"], w_scale=d["gate_up_scale"],
                        act=gdn.GDN_ACT_SILU, gated=True, workspace=ws, stream=stream)
     act = quantise_rows(d["act"], d["fmt"], d["act8"], d["act_scale"], stream=stream)[0]
@@ -277,14 +278,16 @@ def ffn_step(d: dict, stream=None) -> None:
                        residual=d["stream"], workspace=ws, stream=stream)
 
 
-def upload_head(inp: dict, *, fmt: str = "bf16", n_ids: int = 1, top_k: int = 0, logits_dtype=torch.bfloat16) -> dict:
-    """Device tensors of one head_step (workloads.make_head_inputs): stream [M][hidden] fp32, norm_w, the vocabulary's
-    weight w [vocab][hidden] in ``fmt``, logits, and what gdn_logprob answers with; ids int32 [M][n_ids] is the caller's
+def upload_head(inp: dict, *, fmt: str = "bf16", n_ids: int = 1, top_k: int = 0, logits_dtype=torch.bfloat16,
+                eps: float = 1e-6) -> dict:
+    """Device tensors of one head_step (workloads.make_head_inputs): stream [M][hidden] fp32, norm_w and the norm's eps, the
+    vocabulary's weight w [vocab][hidden] in ``fmt``, logits, and what gdn_logprob answers with; ids int32 [M][n_ids] is the caller's
     to fill."""
     f32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda()
     M, hidden = inp["stream"].shape
     V = inp["w"].shape[0]
-    d = {"M": M, "hidden": hidden, "vocab": V, "stream": f32(inp["stream"]), "norm_w": f32(inp["norm_w"])}
+    d = {"M": M, "hidden": hidden, "vocab": V, "stream": f32(inp["stream"]), "norm_w": f32(inp["norm_w"]),
+         "eps": eps}
     d["w"], d["w_scale"] = quantise_rows(f32(inp["w"]).bfloat16(), fmt)
     d["h"] = torch.empty((M, hidden), dtype=torch.uint8 if fmt != "bf16" else torch.bfloat16, device="cuda").view(CODES[fmt])
     d["h_scale"] = None if fmt == "bf16" else torch.empty(M, dtype=torch.float32, device="cuda")
@@ -306,7 +309,7 @@ def head_step(d: dict, temperature: float = 1.0, stream=None) -> dict:
     drafted tokens' log probabilities and ranks, the rows' entropy and their top alternatives."""
     M, V, ws = d["M"], d["vocab"], d["workspace"]
     gdn.gdn_norm(d["stream"][:, None], d["norm_w"], d["h"][:, None], M, scale=None if d["h_scale"] is None else d["h_scale"][:, None],
-                 stream=stream)
+                 eps=d.get("eps", 1e-6), stream=stream)
     gdn.gdn_linear_act(d["h"], d["w"], d["logits"], M, V, d["hidden"], x_scale=d["h_scale"], w_scale=d["w_scale"],
                        workspace=ws, stream=stream)
     gdn.gdn_logprob(d["logits"], M, V, ids=d["ids"], temperature=temperature, workspace=ws, stream=stream, **d["answer"])
