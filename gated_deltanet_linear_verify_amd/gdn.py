@@ -581,6 +581,8 @@ def gdn_norm(x, weight, out, n_tok: int, *, residual=None, total=None, scale=Non
     d, heads = x.shape[-1], x.shape[1] if x.dim() == 3 else 0
     r = [None if t is None else _rows(fn, n, t, here, T, n_tok, d, n == "out")
          for n, t in (("x", x), ("residual", residual), ("total", total), ("out", out))]
+    if weight is not None and tuple(weight.shape) != (d,):  # one of all heads would be cut to its first d values
+        raise _bad(f"{fn}: weight has shape {tuple(weight.shape)}, expected {(d,)}")
     _check(lib().gdn_norm(r[0], r[1], r[2], None if weight is None else _floats(fn, "weight", weight, here, T, d), r[3],
                           None if scale is None else _floats(fn, "scale", scale, here, T, n_tok, heads), d, n_tok, eps, mode,
                           T.stream(stream, here)))
