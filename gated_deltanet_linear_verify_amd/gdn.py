@@ -598,9 +598,14 @@ def gdn_linear_act_workspace_bytes(M: int, N: int, K: int, dtype, gated: bool = 
 def gdn_linear_act(x, w, out, M: int, N: int, K: int, *, x_scale=None, w_scale=None, bias=None, act: int = GDN_ACT_NONE,
                    gated: bool = False, residual=None, workspace=None, stream=None) -> None:
     """out [M][N] = act(x w^T + bias) + residual, or act(gate) * up of w's first and last N rows where gated; x [M][K] and
-    w [N or 2 N][K] in bfloat16, or float8_e4m3fn or int8 with float32 scales per row."""
+    w [N or 2 N][K] in bfloat16, or float8_e4m3fn or int8 with float32 scales per row.  w and bias may have more rows where not
+    gated; those are left alone."""
     fn, T, rows = "gdn_linear_act", _torch(), 2 * N if gated else N
     here = T.device()
+    if gated:  # of more rows the up rows would be taken from among the gate's
+        for name, t in (("w", w), ("w_scale", w_scale), ("bias", bias)):
+            if t is not None and t.shape[0] != rows:
+                raise _bad(f"{fn}: {name} has {t.shape[0]} rows, a gated product of {N} columns takes {rows}")
     ws, ws_bytes = _scratch(fn, workspace, here)
     _check(lib().gdn_linear_act(
         _mat(fn, "x", x, here, T, M, K, T.all, x_scale), _mat(fn, "w", w, here, T, rows, K, T.all, w_scale), M, N, K,
