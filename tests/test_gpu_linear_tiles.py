@@ -39,8 +39,8 @@ SIZES = [
     (2305, 5505, 336, "e4m3", False), (769, 5121, 5136, "bf16", False), (769, 2564, 5136, "bf16", True), (1023, 5121, 13_840, "i8", False),
     (1025, 2564, 13_840, "e4m3", True),
 ]
-# with an out in bf16 the 8-bit products of a sum are kept to about 16 bits of the largest beside them
-E4M3_SUMS = 2.0 ** -15
+# with an out in bf16, of eight neighbouring products all but the largest are cut at 2^-13 of it
+E4M3_SUMS = 7 * 2.0 ** -13
 
 
 def repeat(s, M):
