@@ -17,9 +17,9 @@
 // 131072 allowed beside -1e10, top 20: 1024 rows 58 us, and 53 beside -infinity; one row 11 and 8, and 11 and 5 for the join; one
 // alternative at a time took 50 times as long).  Slices of one row meet in the workspace, where a second kernel joins them.
 //
-// 1024 x 131071 bf16 with a token and 20 alternatives each: 67 us, 4.0 TB/s (a plain read 5.65); the vector unit issues for 79%
+// 1024 x 131071 bf16 with a token and 20 alternatives each: 68 us, 3.9 TB/s (a plain read 5.65); the vector unit issues for 78%
 // of the time: 8.5 instructions a logit (unpacking 1, the chunks' maxima 1.5, the exponent 1, the power 2, the sums 3).
-// One row of 131072: 6.7 us and 6.0 for the join.
+// One row of 131072: 6.8 us and 6.1 for the join.
 #include <algorithm>
 
 #include "gdn_rows.h"

@@ -638,13 +638,17 @@ enum gdn_act {
  * product toward zero at 2^-13 of the largest one's power of two: p is off by less than 7 2^-13 of the sum of its products'
  * sizes, which is less than half of what bf16's rounding of that sum would be (1.6e-4 of it for codes spread over eight
  * binades; 1.4e-5 of the result's norm for normal values).  With a GDN_F32 out the codes are widened first, and products exact.
+ * x.scale[m] w.scale[n] is rounded to fp32 before it meets the sum, and has to be in its range.  SiLU and sigmoid may be 0 where
+ * they are below 2^-120, and GELU is off by up to 2^-22 |v| for a negative v, as 1 + erf is.
  * The order of a sum, and with it the last bits, may differ between sizes, not between calls.  bias (fp32) and
  * residual may be NULL.  out and residual [M][N] are GDN_F32 or GDN_BF16, aligned to their elements; residual may be
  * out itself (same stride and type), otherwise nothing may overlap out.
  *   x and w: 16-byte aligned with rows that keep that alignment; K a multiple of 8 (GDN_BF16) or 16 (8 bits), for
  *   GDN_I8 below 2^17.  M >= 0 (0 is a no-op), N, K >= 1, each below 2^26.
  *   workspace: device memory of gdn_linear_act_workspace_bytes (NULL where that is 0), 16-byte aligned, needs no
- *   initialisation; calls (and recorded graphs) that may run at the same time need one each.
+ *   initialisation; calls (and recorded graphs) that may run at the same time need one each.  A call of fewer rows may need more.
+ * gdn_linear computes the same for GDN_BF16 and K in whole 64s, into up to four outputs at once.  For one output this takes as
+ * long up to 16 rows (within 5%, less where K is cut into parts) and from 2% to 37% less beyond.
  * Errors: NULL, misalignment, scales missing or given for the wrong type, out's rows on top of each other, out on
  * residual's memory with another stride or type, a workspace that is missing or too small, unknown act -> GDN_ERR_ARG;
  * sizes -> GDN_ERR_SHAPE; M < 0 -> GDN_ERR_RANGE; types -> GDN_ERR_DTYPE.
@@ -668,8 +672,9 @@ size_t gdn_linear_act_workspace_bytes(int32_t M, int32_t N, int32_t K, int32_t d
  * probabilities -infinity and entropy 0.  A row that holds a NaN or +infinity has NaN for lse, entropy and the log
  * probabilities of valid tokens.  Every output is optional (NULL); logprob and rank need ids, and top_ids and top_logprob come together.
  * Sums are in fp32.  Every logit is read once, beside those of the given tokens; up to twice where very many are equal to
- * one of the alternatives (a finite mask over most of a row) or where log2(e) / T times the largest is beyond 2^30, and in a row
- * with a NaN or +infinity once more for each given token and each alternative.
+ * one of the alternatives (a finite mask over most of a row) or where log2(e) / T times the largest is beyond 2^30.  Once more for
+ * each given token and each alternative in a row with a NaN or +infinity, and for each alternative where those recur in the same
+ * 16 bytes of every 4 KiB.
  *   logits: aligned to their elements, any row stride.  n_rows 0 .. 2^26 (0 is a no-op); n_vocab 1 .. 2^24;
  *   n_ids 0 .. 64; top_k 0 .. min(64, n_vocab); temperature: from 2^-20 to 2^20.
  *   workspace: as gdn_linear_act's, of gdn_logprob_workspace_bytes.
