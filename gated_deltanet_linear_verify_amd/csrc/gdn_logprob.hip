@@ -293,10 +293,18 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
         closed = true;
         wide = false;
     };
+    // A batch is summed by itself (up to 64 logits a thread) before it joins the sums: one chain of additions over a long row of
+    // equal logits would round the same way at each (2^22 of them: off by 2e-4).
+    float bs = 0.0f, bu = 0.0f;
     auto add = [&](float x) {
         const float d = __builtin_fmaf(x, c2, -sum.k), e = __builtin_amdgcn_exp2f(d);
-        sum.s += e;
-        sum.u = __builtin_fmaf(e, fmaxf(d, -1e30f), sum.u);  // a masked logit's e is 0, but not its d
+        bs += e;
+        bu = __builtin_fmaf(e, fmaxf(d, -1e30f), bu);  // a masked logit's e is 0, but not its d
+    };
+    auto join = [&] {
+        sum.s += bs;
+        sum.u += bu;
+        bs = bu = 0.0f;
     };
     // The logits of the listed chunks that reach the bar, and what was kept, ordered: all threads, between barriers.
     // Those of -infinity are not listed.  The head's come first, as its indexes do, and the tail's last.
@@ -359,6 +367,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
     for (int i = 0; i < CH; ++i) load(c0, i);
     sum.k = fmaxf(sum.k, rintf(single * c2));
     add(single);
+    join();
     __syncthreads();
     if (extra >= 0)
         for (int k = 0; k < a.n_ids; ++k) {
@@ -472,6 +481,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
             for (int j = 0; j < E; ++j) add(x[j]);
             load(b0 + kBatch, i);
         }
+        join();
     }
 
     tid = own_index();
