@@ -10,6 +10,9 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------------------------
 // bf16 <-> f32.  bf16 is the top half of an f32; f32 -> bf16 rounds to nearest, ties to even.
@@ -94,6 +97,15 @@ __device__ __forceinline__ void lds_dma16(const void *g, void *lds)
     (void)lds;
 #endif
 }
+
+// s_waitcnt immediate: at most n vector-memory operations outstanding (vmcnt bits 3:0 and 15:14;
+// expcnt and lgkmcnt left at their maxima).
+constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
+
+// Scheduling groups (__builtin_amdgcn_sched_group_barrier): n instructions of one kind, groups
+// placed in the order of the calls within the enclosing block.
+constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;
+#define sched_group(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
 // Workgroup barrier for data exchanged through LDS by ds_read / ds_write: waits for this wave's
 // own LDS operations, then meets the other waves.  No wait on the vector-memory counter, so

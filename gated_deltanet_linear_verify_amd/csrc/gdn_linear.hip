@@ -22,13 +22,8 @@
 
 namespace gdn {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-
 constexpr int kLBK = 64;  // k depth of a tile
 
-// s_waitcnt immediate: at most n vector-memory operations outstanding (vmcnt bits 3:0 and 15:14;
-// expcnt and lgkmcnt left at their maxima).
-constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
 constexpr int kLChunks = kLBK / 8;  // 16-byte chunks per tile row
 
 __device__ __forceinline__ f4 mfma_bf16(bf16x8_t a, bf16x8_t b, f4 c)
@@ -41,11 +36,6 @@ __device__ __forceinline__ f4 mfma_bf16(bf16x8_t a, bf16x8_t b, f4 c)
     return c;
 #endif
 }
-
-// Scheduling groups (__builtin_amdgcn_sched_group_barrier): n instructions of one kind, groups
-// placed in the order of the calls within the enclosing block.
-constexpr int kSchedMfma = 0x008, kSchedDsRead = 0x100;
-#define sched_group(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
 
 // LDS byte offset of chunk c of tile row r
 __device__ __forceinline__ int lchunk(int r, int c) { return (r * kLChunks + (c ^ (r & 7))) * 16; }

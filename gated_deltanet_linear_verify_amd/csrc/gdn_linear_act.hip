@@ -22,8 +22,6 @@ namespace gdn {
 
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef int i4 __attribute__((ext_vector_type(4)));
 typedef int i8v __attribute__((ext_vector_type(8)));
 
@@ -215,8 +213,6 @@ __device__ __forceinline__ int64_t weight_row(const LinearActArgs &a, int n0, in
 // ------------------------------------------------------------------------------------------------ tiles
 __device__ __forceinline__ int chunk_at(int r, int c) { return (r * kChunks + (c ^ (r >> 1 & 7))) * 16; }
 
-constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
-
 // Four sums as they are staged: in fp32, or as they are where parts of K are still to be added (int32 stays exact).
 template <int T, class V>
 __device__ __forceinline__ f4 staged(V a, V b, V c, V d, bool raw)
@@ -225,9 +221,6 @@ __device__ __forceinline__ f4 staged(V a, V b, V c, V d, bool raw)
     return f4{(float)a, (float)b, (float)c, (float)d};
 }
 __host__ __device__ constexpr int64_t quads(int64_t n) { return (n + 3) / 4; }
-
-#define sched_group(mask, n) __builtin_amdgcn_sched_group_barrier((mask), (n), 0)
-constexpr int kSchedMfma = 0x008, kSchedVmem = 0x010, kSchedDsRead = 0x100;
 
 // GM x GN waves, each WM x WN MFMA tiles of 32 x 32 (rows of x by rows of w); NBUF tiles in LDS.
 //

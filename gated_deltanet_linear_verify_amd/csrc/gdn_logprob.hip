@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kThreads, 5) void logprob_slice_kernel(LogprobArgs 
     const unsigned char *body = p + head * kSize;
     const float c2 = a.inv_t * kLog2E;
 
-    // They wait in LDS: kept in registers through the loop they would make others spill.
+    // The single values wait in LDS: kept in registers through the loop they would make others spill.
     const bool in_head = slice == 0 && tid < head, in_tail = slice == slices - 1 && tid >= 64 && tid < 64 + tail;
     auto extra_of = [&](int t) { return in_head ? t : in_tail ? a.V - tail + t - 64 : -1; };
     auto single_of = [&](int t) -> float & { return singles[in_head ? t : 8 + (t & 7)]; };

@@ -790,10 +790,6 @@ constexpr int kScanCompute = kChunk / 16;  // compute waves: one 16-token tile e
 constexpr int kProducers = 4;
 constexpr int kScanThreads = 64 * (kScanCompute + kProducers);
 
-// s_waitcnt immediate: wait until at most n vector-memory operations are outstanding (gfx9
-// encoding: vmcnt bits 3:0 and 15:14; expcnt and lgkmcnt left at their maxima).
-constexpr int vmcnt_imm(int n) { return 0x0F70 | (n & 0xF) | ((n >> 4) << 14); }
-
 template <int D, bool ACT_BF16, bool QKN>
 __global__ __launch_bounds__(kScanThreads) void prefill_scan_kernel(PrefillArgs a)
 {

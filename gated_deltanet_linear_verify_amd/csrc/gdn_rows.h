@@ -7,9 +7,6 @@
 
 namespace gdn {
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f8 __attribute__((ext_vector_type(8)));
 
 // N consecutive elements at element offset i, in fp32 (N = 1, 4 or 8; the address is aligned to
